@@ -1,6 +1,7 @@
-"""B200-native BitLinear forward (BitNet b1.58, W1.58A8).
+"""B200-native BitLinear forward (BitNet b1.58, W1.58A8) and the paged 8-bit key/value
+cache with its attention.
 
-Thin Python binding over the C ABI in ``include/bitnet.h`` (library
+Thin Python binding over the C ABI in ``include/bitnet.h`` and ``include/bitnet_kv.h`` (library
 ``libbitnet_b200.so`` built in-tree by ``ternary_weight_fwd_b200.build``).
 The functions keep the C names; this module only marshals arguments:
 PyTorch tensors are used for device memory and streams, every step of the
@@ -9,6 +10,7 @@ library is missing the call raises.
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -48,6 +50,19 @@ class bitnet_op_t(ctypes.Structure):
                 ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("w0", ctypes.c_void_p),
                 ("gamma0", ctypes.c_void_p), ("w1", ctypes.c_void_p), ("gamma1", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("norm_g", ctypes.c_void_p), ("norm_eps", ctypes.c_float)]
+
+
+class bitnet_kv_cache_t(ctypes.Structure):
+    """The paged cache (mirrors the C struct)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_step", ctypes.c_void_p),
+                ("v_step", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class bitnet_kv_batch_t(ctypes.Structure):
+    """A batch of sequences over the cache (mirrors the C struct)."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("T", ctypes.c_int32)]
 
 
 class BitnetError(RuntimeError):
@@ -95,6 +110,13 @@ def load_library(path: str = LIB_PATH):
         "bitnet_set_wait_limit_ns": ([ctypes.c_uint64], ctypes.c_uint64),
         "bitnet_linear_ex": ([P, I, P, P, F, I64, I64, P, P, I64, P, I, P, P, SZ, P], I),
         "bitnet_ffn_gate_up_ex": ([P, I, P, P, F, I64, I64, P, P, P, P, I64, P, I, P, P, SZ, P], I),
+        "bitnet_rope_table": ([ctypes.c_double, I64, ctypes.c_int32, P, P], I),
+        "bitnet_kv_append": ([ctypes.POINTER(bitnet_kv_cache_t), ctypes.POINTER(bitnet_kv_batch_t), P, P, P, I,
+                              ctypes.c_int32, I64, I64, I64, P, I64, P, I64, P], I),
+        "bitnet_attention": ([ctypes.POINTER(bitnet_kv_cache_t), ctypes.POINTER(bitnet_kv_batch_t), P, I64,
+                              ctypes.c_int32, ctypes.c_int32, F, P, I64, P, SZ, P], I),
+        "bitnet_attention_workspace_size": ([ctypes.c_int32] * 6, SZ),
+        "bitnet_batch_status": ([I, ctypes.POINTER(ctypes.c_int), P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -422,3 +444,180 @@ def bitnet_set_wait_limit_ns(ns: int) -> int:
     if prev == 0:
         raise RuntimeError("could not set the wait limit")
     return prev
+
+
+# ---- paged 8-bit key/value cache and its attention -----------------------------
+ROPE_THETA = 500000.0  # BitNetConfig rope_theta
+
+
+class KVCache(NamedTuple):
+    """The tensors of a paged cache: codes int8 [pages][kv heads][page size][head dim], steps fp32
+    [pages][kv heads]; a key or value is code * step.  Any tuple of the four will do."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_step: torch.Tensor
+    v_step: torch.Tensor
+
+
+def kv_cache(num_pages: int, n_kv_heads: int, head_dim: int, page_size: int, device="cuda") -> KVCache:
+    """An empty cache of num_pages pages of page_size tokens (16, 32, 64 or 128)."""
+    shape = (num_pages, n_kv_heads, page_size, head_dim)
+    return KVCache(torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+
+def _kv_views(cache, page_table, seq_lens, q_start, rows):
+    """The C structs of a cache and a batch, after the checks that need the tensors."""
+    k, v, k_step, v_step = cache
+    dev = k.device
+    for t, dt, name in ((k, torch.int8, "k"), (v, torch.int8, "v"), (k_step, torch.float32, "k_step"),
+                        (v_step, torch.float32, "v_step"), (page_table, torch.int32, "page_table"),
+                        (seq_lens, torch.int32, "seq_lens"), (q_start, torch.int32, "q_start")):
+        if t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"the cache is on {dev}, not on a GPU")
+    pages, hk, size, d = k.shape
+    n = seq_lens.numel()
+    if v.shape != k.shape or k_step.shape != (pages, hk) or v_step.shape != (pages, hk):
+        raise ValueError("k, v and their steps do not belong together")
+    if page_table.dim() != 2 or page_table.shape[0] != n or q_start.numel() != n + 1:
+        raise ValueError("page_table, seq_lens and q_start must describe the same sequences")
+    return (bitnet_kv_cache_t(k.data_ptr(), v.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), pages, hk, size, d),
+            bitnet_kv_batch_t(page_table.data_ptr(), seq_lens.data_ptr(), q_start.data_ptr(), page_table.shape[1], n,
+                              rows))
+
+
+def _kv_rows(t, name, like, heads, dtype=None):
+    """Row stride of [T][heads][head dim] rows whose heads are contiguous."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    d = like.shape[3]
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T][{heads or 'heads'}][{d}], got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+
+
+def _kv_call(name, dev, stream, made, *args):
+    """Call a C entry on the tensors' device and the given (or that device's current) stream; memory
+    made for the call is kept from reuse until the stream is through with it."""
+    fn = getattr(load_library(), name)
+    if stream is None:
+        s = torch.cuda.current_stream(dev)
+    else:
+        s = stream
+        if s.device != dev:
+            raise ValueError(f"{name}: the stream is on {s.device}, the cache on {dev}")
+        for t in made:
+            t.record_stream(s)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, s.cuda_stream), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s.cuda_stream), name)
+
+
+def bitnet_rope_table(max_pos, head_dim, theta=ROPE_THETA, *, table=None, device="cuda", stream=None):
+    """Rotation table fp32 [max_pos][head_dim]: cosines of a position's angles, then sines."""
+    made = ()
+    if table is None:
+        table = torch.empty((max_pos, head_dim), dtype=torch.float32, device=device)
+        made = (table,)
+    elif table.dtype != torch.float32 or table.shape != (max_pos, head_dim) or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous fp32 [{max_pos}][{head_dim}]")
+    if not table.is_cuda:
+        raise ValueError(f"table is on {table.device}, not on a GPU")
+    _kv_call("bitnet_rope_table", table.device, stream, made, float(theta), max_pos, head_dim, table.data_ptr())
+    return table
+
+
+def bitnet_kv_append(cache, page_table, seq_lens, q_start, k, v, *, q=None, rope=None, q_out=None, stream=None):
+    """Rotate new queries and keys (rope: table of bitnet_rope_table, or None), quantise the new keys and
+    values and write them into the pages of their sequences.  k, v [T][kv heads][head dim] bf16 or fp32,
+    q [T][heads][head dim] of the same type or None.  seq_lens counts the new tokens.  Returns q_out, the
+    rotated queries in bf16 (None without q)."""
+    kc = cache[0]
+    ks = _kv_rows(k, "k", kc, kc.shape[1])
+    vs = _kv_rows(v, "v", kc, kc.shape[1], k.dtype)
+    rows = k.shape[0]
+    if v.shape[0] != rows:
+        raise ValueError("k and v must have the same rows")
+    c, b = _kv_views(cache, page_table, seq_lens, q_start, rows)
+    qp = op = rp = None
+    heads = qs = os_ = rope_len = 0
+    made = ()
+    if q is not None:
+        qs = _kv_rows(q, "q", kc, None, k.dtype)
+        heads = q.shape[1]
+        if q.shape[0] != rows:
+            raise ValueError("q and k must have the same rows")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            made = (q_out,)
+        os_ = _kv_rows(q_out, "q_out", kc, heads, torch.bfloat16)
+        if q_out.shape[0] != rows:
+            raise ValueError("q_out and q must have the same rows")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope is not None:
+        if rope.dtype != torch.float32:
+            raise TypeError(f"rope must be float32, got {rope.dtype}")
+        if rope.dim() != 2 or rope.shape[1] != kc.shape[3] or not rope.is_contiguous() or rope.device != kc.device:
+            raise ValueError(f"rope must be contiguous [positions][{kc.shape[3]}] on {kc.device}")
+        rp, rope_len = rope.data_ptr(), rope.shape[0]
+    _kv_call("bitnet_kv_append", kc.device, stream, made, c, b, qp, k.data_ptr(), v.data_ptr(), _dtype_code(k), heads,
+             qs, ks, vs, rp, rope_len, op, os_)
+    return q_out
+
+
+def bitnet_attention_workspace_size(n_seqs: int, rows: int, heads: int, kv_heads: int, head_dim: int,
+                                    max_new: int) -> int:
+    return load_library().bitnet_attention_workspace_size(n_seqs, rows, heads, kv_heads, head_dim, max_new)
+
+
+def bitnet_attention(cache, page_table, seq_lens, q_start, q, max_new, *, scale=None, out=None, workspace=None,
+                     stream=None):
+    """Causal grouped-query attention of the new tokens' queries q [T][heads][head dim] bf16 over the cache;
+    max_new: at least the most new tokens of a sequence.  Returns out [T][heads][head dim] bf16 (rows of no
+    sequence are left as they were)."""
+    kc = cache[0]
+    qs = _kv_rows(q, "q", kc, None, torch.bfloat16)
+    rows, heads, d = q.shape
+    c, b = _kv_views(cache, page_table, seq_lens, q_start, rows)
+    made = ()
+    if out is None:
+        out = torch.empty((rows, heads, d), dtype=torch.bfloat16, device=q.device)
+        made = (out,)
+    os_ = _kv_rows(out, "out", kc, heads, torch.bfloat16)
+    if out.shape[0] != rows:
+        raise ValueError("out and q must have the same rows")
+    if workspace is None:
+        need = load_library().bitnet_attention_workspace_size(b.n_seqs, rows, heads, c.n_kv_heads, d, max_new)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        made += (workspace,)
+    elif workspace.device != q.device:
+        raise ValueError(f"workspace is on {workspace.device}, the cache on {q.device}")
+    _kv_call("bitnet_attention", kc.device, stream, made, c, b, q.data_ptr(), qs, heads, max_new,
+             d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
+    return out
+
+
+def bitnet_batch_status(clear=True, stream=None) -> int:
+    """Batch status word of the current device: 0, or BITNET_ERR_INVALID_ARG once a cache call met a page id,
+    length, offset or position out of range.  Synchronises the stream."""
+    out = ctypes.c_int(0)
+    _check(load_library().bitnet_batch_status(1 if clear else 0, ctypes.byref(out), _stream(stream)),
+           "bitnet_batch_status")
+    return out.value

@@ -1,6 +1,6 @@
 """Build the CUDA library libbitnet_b200.so in-tree (sm_100a only).
 
-One translation unit (csrc/bitnet.cu) compiled by nvcc for
+One translation unit (csrc/library.cu, which includes the others) compiled by nvcc for
 arch=compute_100a,code=sm_100a, linked against the shared CUDA runtime so the
 library and PyTorch use one runtime instance (same current device, streams).
 """
@@ -17,7 +17,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
 def sources():
-    out = [os.path.join(INCLUDE, "bitnet.h")]
+    out = [os.path.join(INCLUDE, f) for f in sorted(os.listdir(INCLUDE)) if f.endswith(".h")]
     for f in sorted(os.listdir(CSRC)):
         if f.endswith((".cu", ".cuh", ".h")):
             out.append(os.path.join(CSRC, f))
@@ -28,7 +28,7 @@ def nvcc_cmd(out, extra=()):
     return [NVCC, "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
             "-shared", "-Xcompiler", "-fPIC", "-cudart", "shared",
             "-Xlinker", "-rpath=/usr/local/cuda/lib64",
-            "-I", INCLUDE, "-I", CSRC, *extra, "-o", out, os.path.join(CSRC, "bitnet.cu")]
+            "-I", INCLUDE, "-I", CSRC, *extra, "-o", out, os.path.join(CSRC, "library.cu")]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
