@@ -199,7 +199,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                        const AttnArgs a)
 {
     constexpr int NT = D / 8;               // output column tiles
-    constexpr int KST = D / 16;             // contraction steps of q . k
     constexpr int ROWS = 16 * MT;
     constexpr uint32_t TILE = AT_CHUNK * D; // bytes of K (or V) per stage
     constexpr int QROW = 2 * D + 16;        // bytes of a query row in shared memory

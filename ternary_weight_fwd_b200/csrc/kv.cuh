@@ -4,6 +4,7 @@
 #pragma once
 
 #include "bitnet_kv.h"
+#include "attention_prompt.cuh"
 #include "attention_tokens.cuh"
 #include "kv_append.cuh"
 
@@ -97,7 +98,7 @@ bool encode_codes(CUtensorMap *map, const int8_t *codes, int64_t num_pages, int 
 // ---- attention: choice of kernel and workspace ----------------------------------
 struct AttnPlan {
     bool ok;
-    int mt; // row tiles of 16 of the kernel for few tokens
+    int mt; // row tiles of 16 of the kernel for few tokens; 0: the kernel for prompts
     size_t base_bytes, ml_bytes, part_bytes;
     size_t total() const { return base_bytes + ml_bytes + part_bytes; }
 };
@@ -109,11 +110,11 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d
         n_heads % hk != 0 || n_heads / hk > kMaxGroup || (d != 64 && d != 128) || max_new < 1 || max_new > T)
         return p;
     const int64_t rows = n_heads / hk * max_new;
-    if (rows > AT_MAX_ROWS) return p;
-    p.mt = rows <= 16 ? 1 : 2;
+    p.mt = rows <= 16 ? 1 : rows <= AT_MAX_ROWS ? 2 : 0;
+    const size_t part_rows = (size_t)2 * AT_MAX_CTAS * (p.mt ? 16 * p.mt : AP_ROWS);
     p.base_bytes = align_up((size_t)(n_seqs + 1) * 8, 256);
-    p.ml_bytes = align_up((size_t)2 * AT_MAX_CTAS * 16 * p.mt * sizeof(float2), 256);
-    p.part_bytes = (size_t)2 * AT_MAX_CTAS * 16 * p.mt * d * sizeof(float);
+    p.ml_bytes = align_up(part_rows * sizeof(float2), 256);
+    p.part_bytes = part_rows * d * sizeof(float);
     p.ok = true;
     return p;
 }
@@ -130,6 +131,23 @@ cudaError_t launch_tokens(const CUtensorMap &tk, const CUtensorMap &tv, const At
     if (e == cudaSuccess)
         e = launch_pdl(k_attention_join<D>, dim3((unsigned)(a.bt.n_seqs * a.kv.hk), (unsigned)cdiv(rows, 4)),
                        dim3(128), 0, stream, a, 16 * MT, ctas);
+    return e;
+}
+
+template <int D>
+cudaError_t launch_prompt(const CUtensorMap &tk, const CUtensorMap &tv, const AttnArgs &a, int ctas,
+                          cudaStream_t stream, int dev)
+{
+    static std::atomic<int> done[kMaxDevices];
+    constexpr int smem = ap_smem(D);
+    cudaError_t e = ensure_smem(k_attention_prompt<D>, smem, done, dev);
+    if (e == cudaSuccess) e = launch_pdl(k_attention_plan, dim3(1), dim3(1024), 0, stream, a);
+    if (e == cudaSuccess)
+        e = launch_pdl(k_attention_prompt<D>, dim3(ctas), dim3(AP_THREADS), smem, stream, tk, tv, a);
+    if (e == cudaSuccess)
+        e = launch_pdl(k_attention_prompt_join<D>,
+                       dim3((unsigned)((int64_t)a.bt.T * a.group / AP_ROWS + a.bt.n_seqs), (unsigned)a.kv.hk, D / 16),
+                       dim3(256), 0, stream, a, ctas);
     return e;
 }
 
@@ -250,7 +268,9 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
     const int ctas = std::min(sms, AT_MAX_CTAS);
     const int rows = a.group * max_new;
     cudaError_t e;
-    if (d == 128)
+    if (p.mt == 0)
+        e = d == 128 ? launch_prompt<128>(tk, tv, a, ctas, stream, dev) : launch_prompt<64>(tk, tv, a, ctas, stream, dev);
+    else if (d == 128)
         e = p.mt == 1 ? launch_tokens<128, 1>(tk, tv, a, ctas, rows, stream, dev)
                       : launch_tokens<128, 2>(tk, tv, a, ctas, rows, stream, dev);
     else

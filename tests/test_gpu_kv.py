@@ -229,3 +229,65 @@ def test_tokens_same_bits_every_time():
     a = check_attention(b, cache, 12, 128, 141)
     for _ in range(3):
         assert same_bits(a, check_attention(b, cache, 12, 128, 141))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_lengths(page, d):
+    """Whole prompts and chunks of lengths around rows, tiles, blocks and pages; sequences without new
+    tokens, with fewer cached than new tokens, with none."""
+    new = [40, 1, 0, 63, 64, 65, 130, 200, 5, 3, 33]
+    lens = [40, 300, 7, 63, 64, 200, 130, 333, 3, 0, 128]
+    b = make_batch(new, lens, page, page + d + 1, behind=2)
+    cache = make_cache(b["pages"], 2, page, d, page * d + 2, b["free"])
+    check_attention(b, cache, 8, d, 151)
+
+
+@pytest.mark.parametrize("hq,hk", [(20, 5), (1, 1), (3, 3), (7, 1), (32, 1), (12, 4), (128, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_heads(hq, hk, d):
+    """Groups of any size, those that do not divide a row tile among them."""
+    new, lens = [37, 150, 2], [37, 190, 500]
+    b = make_batch(new, lens, 64, hq)
+    check_attention(b, make_cache(b["pages"], hk, 64, d, hq, b["free"]), hq, d, 161, max_new=150)
+
+
+@pytest.mark.parametrize("n,length,hq,hk", [(1000, 1000, 4, 1), (64, 5000, 4, 2), (700, 2111, 5, 5)])
+def test_prompt_long(n, length, hq, hk):
+    """Tiles shared by several CTAs."""
+    b = make_batch([n], [length], 32, n)
+    check_attention(b, make_cache(b["pages"], hk, 32, 128, n + 1, b["free"]), hq, 128, 171)
+
+
+def test_prompt_many_sequences():
+    r = np.random.default_rng(31)
+    new = r.integers(0, 60, 300).tolist()
+    lens = [n + int(r.integers(0, 90)) for n in new]
+    b = make_batch(new, lens, 16, 32, behind=1)
+    check_attention(b, make_cache(b["pages"], 1, 16, 64, 33, b["free"]), 1, 64, 172)
+
+
+@pytest.mark.parametrize("qscale", [0.0, 1e-30, 1e-3, 30.0, 1e4])
+def test_prompt_query_range(qscale):
+    b = make_batch([50, 20], [200, 20], 16, 34)
+    check_attention(b, make_cache(b["pages"], 1, 16, 128, 35, b["free"]), 4, 128, 181, qscale=qscale, scale=0.01)
+
+
+def test_prompt_steps_of_any_size():
+    """Steps of neighbouring pages up to nine orders of magnitude apart, pages of zeros."""
+    b = make_batch([90, 60], [400, 290], 16, 36)
+    cache = make_cache(b["pages"], 1, 16, 128, 37, b["free"])
+    r = np.random.default_rng(38)
+    cache[3][:] = (10.0 ** r.uniform(-6, 3, cache[3].shape)).astype(np.float32)
+    cache[3][b["table"][0, :3]] = 0.0
+    cache[2][b["table"][1, 2:5]] = 0.0
+    cache[3][b["table"][1, :8]] = 0.0  # a whole first block of zeros
+    check_attention(b, cache, 4, 128, 182)
+
+
+def test_prompt_same_bits_every_time():
+    b = make_batch([300, 1, 77, 512], [900, 1, 77, 2048], 32, 39)
+    cache = make_cache(b["pages"], 3, 32, 128, 40, b["free"])
+    a = check_attention(b, cache, 12, 128, 191)
+    for _ in range(3):
+        assert same_bits(a, check_attention(b, cache, 12, 128, 191))
