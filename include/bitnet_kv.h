@@ -27,7 +27,7 @@
  *               of q, k, v and out, at positions seq_lens[b] - n_b ..
  *               seq_lens[b] - 1 (n_b = q_start[b + 1] - q_start[b], which may
  *               be 0).  Rows outside [q_start[0], q_start[n_seqs]) (padding)
- *               are neither read nor written.
+ *               are not written, and what they hold has no effect.
  *
  * The conventions of bitnet.h hold (device pointers, caller-owned memory, no
  * allocation, no synchronisation, host-side validation before any launch,

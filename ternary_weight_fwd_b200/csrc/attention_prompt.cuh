@@ -6,62 +6,77 @@
 // exponentials: 4 D flops and one exp2 per visible (query head, token) pair.
 //
 // Query rows of a (sequence, kv head) are its new tokens times the query heads
-// of the group (row = token * group + head), cut into tiles of 256 rows: two MMA
-// tiles A and B of 128, so that one's softmax runs while the other's products
-// do.  Tokens are taken in blocks of 128.  The work is the list of all
-// (sequence, kv head, row tile, block that the tile sees), cut into equal
-// contiguous shares, one per CTA (one CTA per SM); tiles that two or more CTAs
-// share are joined by k_attention_prompt_join through the workspace, in the
-// order of the CTAs.
+// of the group (row = token * group + head).  An MMA tile holds as many whole
+// tokens as fit its 128 rows, a row tile is two of them, A and B, so that one's
+// softmax runs while the other's products do.  Tokens are taken in blocks of 128.
+// The work is the list of all (sequence, kv head, row tile, block that the tile
+// sees), with two more units per tile for loading its queries and storing its
+// rows, cut into equal contiguous shares, one per CTA (one CTA per SM); tiles
+// that two or more CTAs share are joined by k_attention_prompt_join through the
+// workspace, in the order of the CTAs.
 //
-// One CTA, 16 warps:
-//   warps 0-3, 4-7  softmax of tile A, B: a thread per row.  They load the
-//                   queries (scaled by a power of two per row, fp16, into the
-//                   K-major 128-byte-swizzled layout), read scores from tensor
-//                   memory, write weights back over them as the next product's
-//                   A operand, rescale and finally read the sums.
-//   warps 8-11      int8 codes -> fp16, K and V tiles alike: rows of tokens, in
-//                   the 128-byte-swizzled layout that serves K as a K-major and
-//                   V as an MN-major B operand (a row of V is contiguous in the
-//                   head dimension, the N of that product).
-//   warp 12         TMA of the codes (16-token boxes, one page each)
-//   warp 13         MMA issuer, owner of tensor memory
-// Codes are exact in fp16.  A page's v_step is applied in two factors: a power of
-// two on the code (exact in fp16 down to 2^-24) and the rest, in [1, 2), on the
-// weight; the sums are in units of a power of two near the current pages' steps.
+// One CTA, 24 warps of 80 registers:
+//   warps 0-7, 8-15 softmax of tile A, B: two threads per row, 64 tokens of a block
+//                   each (more warps in flight than a thread per row with 128 scores
+//                   in registers, which was bound by latency).  Weights go back over
+//                   their scores in tensor memory as the A operand of the second
+//                   product; sums are rescaled and finally read there
+//   warps 16-19     widen the int8 codes, rows of tokens in the 128-byte-swizzled
+//                   layout that serves K (bf16) as a K-major and V (fp16) as an
+//                   MN-major B operand (a row of V is contiguous in the head
+//                   dimension, the N of that product)
+//   warp 20         TMA of the codes (16-token boxes, one page each); steps
+//   warp 21         MMA issuer, owner of tensor memory
+//   warp 22         queries, as they are (bf16), by TMA
+//   warp 23         walks the unit list and hands out the tiles
+// Codes are exact in bf16 and in fp16.  Weights are fp16 and carry v_step: its
+// power of two goes on the codes (exact in fp16 down to 2^-24), the rest, in
+// [1, 2), into the weight's exponent as its logarithm; the sums are in units of a
+// power of two near the current pages' steps.
 #pragma once
 
 #include "attention_tokens.cuh"
 
 namespace bitnet {
 
-constexpr int AP_ROWS = 256;      // query rows per tile (two MMA tiles)
+constexpr int AP_ROWS = 256;      // query rows per tile (two MMA tiles), some of them dead
 constexpr int AP_BLOCK = 128;     // tokens per block
-constexpr int AP_THREADS = 512;
+constexpr int AP_THREADS = 768;
 constexpr int AP_RAW = 3;         // ring of int8 tiles
 constexpr int AP_CONV = 3;        // ring of fp16 tiles
 constexpr int AP_STEPS = 4;       // ring of blocks' steps (see the producer)
-constexpr int AP_MIN_UNITS = 2;   // blocks worth a CTA of their own
-constexpr int AP_CONV_WARP0 = 8, AP_TMA_WARP = 12, AP_MMA_WARP = 13;
+constexpr int AP_OVER = 2;         // units that a tile costs besides its blocks
+constexpr int AP_MIN_UNITS = 4;    // units worth a CTA of their own
+constexpr int AP_SEGS = 4;        // ring of tiles handed out
+constexpr int AP_CONV_WARP0 = 16, AP_TMA_WARP = 20, AP_MMA_WARP = 21, AP_Q_WARP = 22, AP_SCHED_WARP = 23;
+constexpr int AP_SEG_READERS = 23; // warps that read every tile's description
 constexpr float AP_LAZY = 8.0f;   // the reference of a row's exponents lags its maximum by up to 2^8
 
+constexpr int AP_HDR = 6144;      // barriers, steps, tiles, maxima on their way
 constexpr __host__ __device__ int ap_smem(int d)
 {
-    return 1024 + 2 * 128 * d * 2 + AP_CONV * AP_BLOCK * d * 2 + AP_RAW * AP_BLOCK * d + 1024;
+    return AP_HDR + 2 * 128 * d * 2 + AP_CONV * AP_BLOCK * d * 2 + AP_RAW * AP_BLOCK * d + 1024;
 }
 
-// Blocks that row tile qt of a sequence sees (rows see tokens 0 .. len - n + row / group).
+// Tokens of one MMA tile.
+constexpr __host__ __device__ int ap_tokens(int group) { return 128 / group; }
+
+// Blocks that row tile qt of a sequence sees (new token i sees tokens 0 .. len - n + i).
 BITNET_DEVINL int ap_blocks(const AttnSeq &s, int group, int qt)
 {
-    const int last = min(s.n - 1, (int)(((int64_t)(qt + 1) * AP_ROWS - 1) / group));
+    const int last = min(s.n, (qt + 1) * 2 * ap_tokens(group)) - 1;
     const int lim = s.len - s.n + last;
     return lim < 0 ? 0 : lim / AP_BLOCK + 1;
 }
 
 BITNET_DEVINL int ap_tiles(const AttnSeq &s, int group)
 {
-    return (int)(((int64_t)s.n * group + AP_ROWS - 1) / AP_ROWS);
+    const int t = 2 * ap_tokens(group);
+    return (s.n + t - 1) / t;
 }
+
+// Units of a tile: its blocks, behind AP_OVER for loading its queries and storing its rows.
+BITNET_DEVINL int ap_units(int blocks) { return blocks > 0 ? blocks + AP_OVER : 0; }
 
 BITNET_DEVINL int64_t ap_active(int64_t units, int ctas)
 {
@@ -82,7 +97,7 @@ __global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a)
         const AttnSeq s = attn_seq(a, b);
         const int nt = ap_tiles(s, a.group);
         int64_t sum = 0;
-        for (int t = lane; t < nt; t += 32) sum += ap_blocks(s, a.group, t);
+        for (int t = lane; t < nt; t += 32) sum += ap_units(ap_blocks(s, a.group, t));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) a.base[b + 1] = sum * a.kv.hk;
@@ -111,14 +126,15 @@ __global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a)
     }
 }
 
-// Position in the unit list, advanced tile by tile.  Whole warps run it.
+// Walks the unit list tile by tile.  A whole warp runs it.
 struct ApIter {
     int b, h, qt, nt;
-    int j0, cnt, nkv; // blocks [j0, j0 + cnt) of the tile's nkv
+    int nkv;       // blocks that the tile sees
+    int64_t first; // the tile's first unit
     AttnSeq s;
 
     // the tile that holds unit u
-    BITNET_DEVINL void seek(const AttnArgs &a, int64_t u, int64_t u1)
+    BITNET_DEVINL void seek(const AttnArgs &a, int64_t u)
     {
         const int lane = threadIdx.x & 31;
         int lo = 0, hi = a.bt.n_seqs; // base[lo] <= u < base[hi]
@@ -132,14 +148,14 @@ struct ApIter {
         b = lo;
         s = attn_seq(a, b);
         nt = ap_tiles(s, a.group);
-        const int64_t first = a.base[b], per_head = (a.base[b + 1] - first) / a.kv.hk;
-        h = (int)((u - first) / per_head);
-        int64_t rel = (u - first) - h * per_head;
+        const int64_t base = a.base[b], per_head = (a.base[b + 1] - base) / a.kv.hk;
+        h = (int)((u - base) / per_head);
+        first = base + h * per_head;
         qt = 0;
         nkv = 0;
-        j0 = 0;
         for (int t0 = 0; t0 < nt; t0 += 32) {
-            const int mine = t0 + lane < nt ? ap_blocks(s, a.group, t0 + lane) : 0;
+            const int blocks = t0 + lane < nt ? ap_blocks(s, a.group, t0 + lane) : 0;
+            const int mine = ap_units(blocks);
             int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -147,44 +163,61 @@ struct ApIter {
                 if (lane >= o) incl += up;
             }
             const int all = __shfl_sync(0xffffffffu, incl, 31);
-            if (rel < all) {
-                const int at = __ffs(__ballot_sync(0xffffffffu, rel < incl)) - 1;
+            if (u < first + all) {
+                const int at = __ffs(__ballot_sync(0xffffffffu, u < first + incl)) - 1;
                 qt = t0 + at;
-                nkv = __shfl_sync(0xffffffffu, mine, at);
-                j0 = (int)rel - (__shfl_sync(0xffffffffu, incl, at) - nkv);
+                nkv = __shfl_sync(0xffffffffu, blocks, at);
+                first += __shfl_sync(0xffffffffu, incl - mine, at);
                 break;
             }
-            rel -= all;
+            first += all;
         }
-        cnt = (int)min((int64_t)(nkv - j0), u1 - u);
     }
 
-    // the next tile that sees anything; u: its first unit (< u1)
-    BITNET_DEVINL void next(const AttnArgs &a, int64_t u, int64_t u1)
+    // the next tile that sees anything, if there is one
+    BITNET_DEVINL void next(const AttnArgs &a)
     {
+        first += ap_units(nkv);
         do {
             if (++qt >= nt) {
                 qt = 0;
                 if (++h >= a.kv.hk) {
                     h = 0;
                     do {
-                        ++b;
+                        if (++b >= a.bt.n_seqs) return;
                         s = attn_seq(a, b);
                         nt = ap_tiles(s, a.group);
-                    } while (nt == 0 && b + 1 < a.bt.n_seqs);
+                    } while (nt == 0);
                 }
             }
-            nkv = nt > 0 ? ap_blocks(s, a.group, qt) : 0;
-        } while (nkv == 0 && b + 1 < a.bt.n_seqs);
-        j0 = 0;
-        cnt = (int)min((int64_t)nkv, u1 - u);
+            nkv = ap_blocks(s, a.group, qt);
+        } while (nkv == 0);
     }
 };
 
-// kind::f16 instruction descriptor: D fp32, A and B fp16, M = 128.
-constexpr __host__ __device__ uint32_t ap_idesc(int n, bool b_mn_major)
+// One lane of a converged warp, in the form that lets the compiler keep the
+// operands of what it guards in uniform registers.
+BITNET_DEVINL bool elect_one()
 {
-    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The same box into the L2 cache only.
+BITNET_DEVINL void tma_prefetch_3d(const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// kind::f16 instruction descriptor: D fp32, M = 128; A and B bf16 or fp16.
+constexpr __host__ __device__ uint32_t ap_idesc(int n, bool bf16, bool b_mn_major)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
 // MN-major operand, 128-byte swizzle: rows of 64 elements of the M/N dimension,
@@ -244,33 +277,102 @@ BITNET_DEVINL void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
 BITNET_DEVINL int step_exp(float x) { return max((int)((__float_as_uint(x) >> 23) & 0xff) - 127, -126); }
 BITNET_DEVINL float exp2_int(int e) { return __uint_as_float((uint32_t)(max(-126, min(127, e)) + 127) << 23); }
 
-// Unit exponent of the sums from block to block: it moves when the largest step
-// of a block leaves [2^-4, 2^5) of it, and not below 2^-60 of what it was (all
-// roles follow the same rule on the same steps).
 constexpr int AP_NO_UNIT = -1000;
-BITNET_DEVINL int ap_unit(int unit, const float *vs)
+
+// What the other warps need of a block's pages, made by the producer.
+struct ApSteps {
+    float f[8];    // k_step * scale * log2(e), never 0 (scores of masked tokens are -infinity)
+    float lg[8];   // log2 of the part of v_step that the weights carry
+    float inv[8];  // its inverse
+    float mul[8];  // the part that goes on V's codes: a power of two, or 0
+    int unit;      // exponent of the sums' unit from this block on
+    int pad[7];
+};
+
+// A CTA's part of a row tile.
+struct ApSeg {
+    int cnt;         // blocks of this CTA (0: no more tiles)
+    int j0, nkv;     // the first of them; blocks that the tile sees
+    int b, h, qt;
+    int q0, n, len;  // AttnSeq of b
+    int pad[3];
+};
+
+// Two fp32 operations in one instruction.
+BITNET_DEVINL float2 fma2(float2 a, float2 b, float2 c)
 {
-    float mx = 0.0f;
-#pragma unroll
-    for (int i = 0; i < AP_BLOCK / AT_GROUP; ++i) mx = fmaxf(mx, vs[i]);
-    if (!(mx > 0.0f)) return unit;
-    const int e = step_exp(mx);
-    if (unit == AP_NO_UNIT) return e;
-    return e - unit < -4 || e - unit > 4 ? max(e, unit - 60) : unit;
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
-// Power of two that goes on the codes of a page with step v.
-BITNET_DEVINL int ap_code_exp(float v, int unit) { return max(-24, min(5, step_exp(v) - unit)); }
+BITNET_DEVINL float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+BITNET_DEVINL float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Four codes -> two bf16 pairs (bytes 0, 1) and (2, 3): the low seven bits go
+// under the exponent of 128 and 128, or 256 for a negative code, is subtracted.
+BITNET_DEVINL void codes_to_bf16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    constexpr uint32_t k43 = 0x43434343u;
+    const uint32_t low = w & 0x7f7f7f7fu, neg = w & 0x80808080u;
+    const uint32_t a = __byte_perm(low, k43, 0x4140), b = __byte_perm(low, k43, 0x4342);
+    const uint32_t c = __byte_perm(neg, k43, 0x4140), d = __byte_perm(neg, k43, 0x4342);
+    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&c));
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&b),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&d));
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// Four lanes l = 0..3 hold blocks [l][0..3] of four words; afterwards lane l holds [0..3][l].
+BITNET_DEVINL void turn4x4(uint32_t (&o)[4][4], int lane)
+{
+#pragma unroll
+    for (int step = 1; step <= 2; step *= 2) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & step) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { // swap o[i ^ step] of the lower lane with o[i] of the upper one
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? o[i][e] : o[i ^ step][e], step);
+                if (up)
+                    o[i][e] = got;
+                else
+                    o[i ^ step][e] = got;
+            }
+        }
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(AP_THREADS, 1)
     k_attention_prompt(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const AttnArgs a)
+                       const __grid_constant__ CUtensorMap tm_q, const AttnArgs a)
 {
     constexpr uint32_t Q_TILE = 128 * D * 2;        // bytes of one MMA tile's queries
-    constexpr uint32_t C_TILE = AP_BLOCK * D * 2;   // fp16 tile of K or V
+    constexpr uint32_t C_TILE = AP_BLOCK * D * 2;   // 16-bit tile of K or V
     constexpr uint32_t R_TILE = AP_BLOCK * D;       // int8 tile
     constexpr uint32_t SLAB = 128 * 128;            // 64 elements of 128 rows
     constexpr int GROUPS = AP_BLOCK / AT_GROUP;
+    static_assert(384 + AP_STEPS * sizeof(ApSteps) <= 1024 && 1024 + AP_SEGS * sizeof(ApSeg) + 4096 <= AP_HDR, "header");
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
@@ -279,14 +381,20 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     uint64_t *raw_empty = raw_full + AP_RAW;
     uint64_t *cv_full = raw_empty + AP_RAW;
     uint64_t *cv_empty = cv_full + AP_CONV;
-    uint64_t *q_full = cv_empty + AP_CONV; // [2]
-    uint64_t *s_full = q_full + 2;         // [2] scores are in tensor memory
-    uint64_t *p_full = s_full + 2;         // [2] weights are
-    uint64_t *o_full = p_full + 2;         // [2] a tile's sums are complete
-    uint64_t *mma_done = o_full + 2;
+    uint64_t *seg_full = cv_empty + AP_CONV;
+    uint64_t *seg_empty = seg_full + AP_SEGS;
+    uint64_t *q_full = seg_empty + AP_SEGS;
+    uint64_t *q_empty = q_full + 1;        // every product of the queries is complete
+    uint64_t *s_full = q_empty + 1;        // [2] scores are in tensor memory
+    uint64_t *p_full = s_full + 2;         // [2][2] weights of the block's halves are
+    uint64_t *o_full = p_full + 4;         // [2] a tile's sums are complete
+    uint64_t *pair = o_full + 2;           // [8] the two warps of 32 rows exchange a value per row
+    uint64_t *mma_done = pair + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
-    float *s_step = reinterpret_cast<float *>(smem + 512); // [AP_STEPS][2][8]
-    unsigned char *s_q = smem + 1024;
+    ApSteps *s_step = reinterpret_cast<ApSteps *>(smem + 384);              // [AP_STEPS]
+    ApSeg *s_seg = reinterpret_cast<ApSeg *>(smem + 1024);                  // [AP_SEGS]
+    float *s_mx = reinterpret_cast<float *>(smem + 1024 + AP_SEGS * sizeof(ApSeg)); // [2 turns][2 tiles][2 halves][128]
+    unsigned char *s_q = smem + AP_HDR;
     unsigned char *s_conv = s_q + 2 * Q_TILE;
     unsigned char *s_raw = s_conv + AP_CONV * C_TILE;
 
@@ -300,18 +408,26 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             mbar_init(&cv_full[i], 4);
             mbar_init(&cv_empty[i], 1);
         }
+        for (int i = 0; i < AP_SEGS; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], AP_SEG_READERS);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int x = 0; x < 2; ++x) {
-            mbar_init(&q_full[x], 4);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 4);
+            mbar_init(&p_full[2 * x], 4);
+            mbar_init(&p_full[2 * x + 1], 4);
             mbar_init(&o_full[x], 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&pair[i], 2);
         mbar_init(mma_done, 1);
         fence_mbarrier_init();
     }
     if (tid == AP_TMA_WARP * 32) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_q);
     }
     if (warp == AP_MMA_WARP) {
         tmem_alloc(tmem_slot, 512);
@@ -324,28 +440,98 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
 
-    const int64_t total = a.base[a.bt.n_seqs];
-    const int64_t active = ap_active(total, gridDim.x);
-    const bool idle = blockIdx.x >= active;
-    const int64_t u0 = idle ? 0 : total * blockIdx.x / active, u1 = idle ? 0 : total * (blockIdx.x + 1) / active;
-    ApIter it;
-    it.cnt = 0;
-    if (u0 < u1) it.seek(a, u0, u1);
+    // Every wait below is by whole warps; `ok` is the same in all lanes.
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t par) {
+        ok = __all_sync(0xffffffffu, ok && kv_wait(bar, par));
+        return ok;
+    };
+    // the next tile's description (false: no more)
+    uint32_t gslot = 0, gph = 0;
+    ApSeg sg;
+    auto next_seg = [&]() {
+        if (!wait(&seg_full[gslot], gph)) return false;
+        sg = s_seg[gslot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[gslot]);
+        if (++gslot == AP_SEGS) {
+            gslot = 0;
+            gph ^= 1;
+        }
+        return sg.cnt > 0;
+    };
 
-    if (warp == AP_TMA_WARP) {
+    if (warp == AP_SCHED_WARP) {
+        // ---------------- tiles ----------------
+        const int64_t total = a.base[a.bt.n_seqs];
+        const int64_t active = ap_active(total, gridDim.x);
+        const bool idle = blockIdx.x >= active;
+        const int64_t u0 = idle ? 0 : total * blockIdx.x / active, u1 = idle ? 0 : total * (blockIdx.x + 1) / active;
+        ApIter it;
+        it.first = 0;
+        if (u0 < u1) it.seek(a, u0);
+        for (bool more = true; more;) {
+            int j0 = 0, j1 = 0; // this share's blocks of the tile
+            more = false;
+            while (it.first < u1 && !more) {
+                j0 = (int)max((int64_t)0, u0 - it.first - AP_OVER);
+                j1 = (int)min((int64_t)it.nkv, u1 - it.first - AP_OVER);
+                more = j1 > j0;
+                if (!more) it.next(a);
+                if (it.b >= a.bt.n_seqs) break;
+            }
+            if (!wait(&seg_empty[gslot], gph ^ 1)) break;
+            if (lane == 0) {
+                ApSeg &d = s_seg[gslot];
+                d.cnt = more ? j1 - j0 : 0;
+                d.j0 = j0;
+                d.nkv = it.nkv;
+                d.b = it.b;
+                d.h = it.h;
+                d.qt = it.qt;
+                d.q0 = it.s.q0;
+                d.n = it.s.n;
+                d.len = it.s.len;
+                mbar_arrive(&seg_full[gslot]);
+                if (more) { // the queries are on their way to the L2 cache by the time they are asked for
+                    const int tokens = ap_tokens(a.group);
+                    for (int x = 0; x < 2; ++x)
+                        for (int i = 0; i < D / 64; ++i)
+                            tma_prefetch_3d(&tm_q, 64 * i, it.h * a.group, it.s.q0 + (2 * it.qt + x) * tokens);
+                }
+            }
+            __syncwarp();
+            if (++gslot == AP_SEGS) {
+                gslot = 0;
+                gph ^= 1;
+            }
+            if (more) it.next(a);
+            if (it.b >= a.bt.n_seqs) it.first = u1;
+        }
+    } else if (warp == AP_TMA_WARP) {
         // ---------------- producer ----------------
         // Lanes 0-7: the 16-token groups of a block.  Page ids are fetched two blocks and
         // steps one block ahead.  A block's steps go to slot (block % 4): its first copy waits
         // for a raw tile that is free only after the products of the block three before it, so
         // nobody still reads the steps of the block four before.
-        auto fetch = [&](const ApIter &w, int j, int64_t u, int &page, int &row, bool &valid) {
+        int j = 0; // of sg
+        bool more = next_seg();
+        auto fetch = [&](int &page, int &row, bool &valid, bool &head, bool &block) {
             page = -1;
             row = 0;
-            const int key0 = j * AP_BLOCK + lane * AT_GROUP;
-            valid = lane < GROUPS && u < u1 && key0 < w.s.len;
+            valid = false;
+            head = j == 0;
+            block = more;
+            if (!more) return;
+            const int key0 = (sg.j0 + j) * AP_BLOCK + lane * AT_GROUP;
+            valid = lane < GROUPS && key0 < sg.len;
             if (valid) {
-                page = page_of(a.kv, a.bt, w.b, key0 >> a.kv.page_shift);
-                row = (w.h << a.kv.page_shift) + (key0 & ((1 << a.kv.page_shift) - 1));
+                page = page_of(a.kv, a.bt, sg.b, key0 >> a.kv.page_shift);
+                row = (sg.h << a.kv.page_shift) + (key0 & ((1 << a.kv.page_shift) - 1));
+            }
+            if (++j >= sg.cnt) {
+                j = 0;
+                more = next_seg();
             }
         };
         auto steps = [&](int pg, int rw, float &k, float &v) {
@@ -356,40 +542,41 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 v = a.kv.v_step[at];
             }
         };
-        // `ahead` walks two blocks in front
-        ApIter ahead = it;
-        int64_t ua = u0;
-        int ja = 0; // within ahead's blocks
-        auto advance = [&]() {
-            ++ua;
-            if (++ja >= ahead.cnt && ua < u1) {
-                ahead.next(a, ua, u1);
-                ja = 0;
-            }
-        };
         int page, row, page1, row1, page2, row2;
-        bool valid, valid1, valid2;
+        bool valid, valid1, valid2, head, head1, head2, block, block1, block2;
         float ks, vs, ks1, vs1;
-        fetch(ahead, ahead.j0 + ja, ua, page, row, valid);
-        advance();
-        fetch(ahead, ahead.j0 + ja, ua, page1, row1, valid1);
-        advance();
+        fetch(page, row, valid, head, block);
+        fetch(page1, row1, valid1, head1, block1);
         steps(page, row, ks, vs);
-        int stage = 0, slot = 0;
+        int stage = 0, slot = 0, unit = AP_NO_UNIT;
         uint32_t phase = 0, issued = 0, last_par = 0;
-        bool ok = true;
-        for (int64_t u = u0; u < u1 && ok; ++u) {
+        while (block && ok) {
             steps(page1, row1, ks1, vs1);
-            fetch(ahead, ahead.j0 + ja, ua, page2, row2, valid2);
-            advance();
+            fetch(page2, row2, valid2, head2, block2);
+            // The sums' unit moves when the largest step of a block leaves [2^-4, 2^5) of it, and
+            // not below 2^-60 of what it was.
+            if (head) unit = AP_NO_UNIT;
+            const float vmax = warp_max(vs);
+            if (vmax > 0.0f) {
+                const int e = step_exp(vmax);
+                if (unit == AP_NO_UNIT)
+                    unit = e;
+                else if (e - unit < -4 || e - unit > 4)
+                    unit = max(e, unit - 60);
+            }
+            const int ce = max(-24, min(5, step_exp(vs) - unit)); // exponent that goes on the codes
+            const float rest = vs > 0.0f ? vs * exp2_int(-(unit + ce)) : 1.0f;
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, valid && page >= 0)) * AT_GROUP * D;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[stage], phase ^ 1));
-                if (!ok) break;
+                if (!wait(&raw_empty[stage], phase ^ 1)) break;
                 if (kv == 0 && lane < GROUPS) {
-                    s_step[slot * 16 + lane] = ks;
-                    s_step[slot * 16 + 8 + lane] = vs;
+                    ApSteps &st = s_step[slot];
+                    st.f[lane] = fmaxf(a.scale_log2 * ks, 1e-37f);
+                    st.lg[lane] = log2f(rest);
+                    st.inv[lane] = 1.0f / rest;
+                    st.mul[lane] = vs > 0.0f ? exp2_int(ce) : 0.0f;
+                    if (lane == 0) st.unit = unit;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], bytes);
@@ -408,11 +595,15 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             page = page1;
             row = row1;
             valid = valid1;
+            head = head1;
+            block = block1;
             ks = ks1;
             vs = vs1;
             page1 = page2;
             row1 = row2;
             valid1 = valid2;
+            head1 = head2;
+            block1 = block2;
         }
         for (int s = 0; s < AP_RAW; ++s)
             if (issued & (1u << s)) mbar_wait_drain(&raw_full[s], (last_par >> s) & 1);
@@ -420,13 +611,12 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         // ---------------- MMA issuer ----------------
         // Per block: weights of A times V, next scores of A, then the same for B: while one
         // tile's softmax runs the other's products do.
-        constexpr uint32_t id_s = ap_idesc(AP_BLOCK, false), id_o = ap_idesc(D, true);
+        constexpr uint32_t id_s = ap_idesc(AP_BLOCK, true, false), id_o = ap_idesc(D, false, true);
         uint32_t cslot = 0, cphase = 0;
         uint32_t qph = 0, pph[2] = {0, 0};
-        bool ok = true;
         auto scores = [&](int x, uint32_t kslot) {
             const uint64_t ad = umma_desc_k_sw128(s_q + x * Q_TILE), bd = umma_desc_k_sw128(s_conv + kslot * C_TILE);
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = (uint64_t)((k >> 2) * (SLAB >> 4) + (k & 3) * 2);
@@ -436,25 +626,30 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             }
             __syncwarp();
         };
+        // a half's weights lie over the first half of its scores
         auto sums = [&](int x, uint32_t vslot, bool first) {
             const uint64_t bd = umma_desc_mn_sw128(smem_u32(s_conv + vslot * C_TILE), SLAB);
-            if (lane == 0) {
 #pragma unroll
-                for (int k = 0; k < AP_BLOCK / 16; ++k)
-                    umma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, bd + (uint64_t)k * (16 * 128 >> 4), id_o,
-                                !first || k != 0);
+            for (int half = 0; half < 2; ++half) {
+                if (!wait(&p_full[2 * x + half], pph[x])) return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + 64 * half + 8 * k,
+                                    bd + (uint64_t)(4 * half + k) * (16 * 128 >> 4), id_o,
+                                    !first || half != 0 || k != 0);
+                }
+                __syncwarp();
             }
+            pph[x] ^= 1;
+            return true;
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (elect_one()) umma_commit(bar);
             __syncwarp();
         };
-        auto wait = [&](uint64_t *bar, uint32_t par) {
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, par));
-            return ok;
-        };
-        auto release = [&](uint32_t s) {
-            if (lane == 0) umma_commit(&cv_empty[s]);
-            __syncwarp();
-        };
-        auto take = [&](uint32_t &s) { // the next fp16 tile
+        auto take = [&](uint32_t &s) { // the next 16-bit tile
             if (!wait(&cv_full[cslot], cphase)) return false;
             s = cslot;
             if (++cslot == AP_CONV) {
@@ -463,99 +658,104 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             }
             return true;
         };
-        for (int64_t u = u0; u < u1 && ok; u += it.cnt, (u < u1 ? it.next(a, u, u1) : (void)0)) {
-            const int nrow = (int)min((int64_t)AP_ROWS, (int64_t)it.s.n * a.group - (int64_t)it.qt * AP_ROWS);
-            const bool two = nrow > 128;
+        while (ok && next_seg()) {
+            const bool two = sg.n > (2 * sg.qt + 1) * ap_tokens(a.group);
             uint32_t ks, vs;
-            if (!take(ks)) break;
-            tc_fence_after();
-            if (!wait(&q_full[0], qph)) break;
+            if (!take(ks) || !wait(q_full, qph)) break;
+            qph ^= 1;
             tc_fence_after();
             scores(0, ks);
-            if (!wait(&q_full[1], qph)) break;
-            tc_fence_after();
             if (two) scores(1, ks);
-            release(ks);
-            qph ^= 1;
-            for (int j = 0; j < it.cnt && ok; ++j) {
-                const bool more = j + 1 < it.cnt;
-                if (!take(vs)) break;
-                if (!wait(&p_full[0], pph[0])) break;
-                pph[0] ^= 1;
-                tc_fence_after();
-                sums(0, vs, j == 0);
-                if (!more) {
-                    if (lane == 0) {
-                        umma_commit(&o_full[0]);
-                        if (!two) umma_commit(&o_full[1]);
-                    }
-                    __syncwarp();
-                }
+            commit(&cv_empty[ks]);
+            if (sg.cnt == 1) commit(q_empty);
+            for (int j = 0; j < sg.cnt && ok; ++j) {
+                const bool more = j + 1 < sg.cnt;
+                if (!take(vs) || !sums(0, vs, j == 0)) break;
                 if (more) {
                     if (!take(ks)) break;
                     tc_fence_after();
                     scores(0, ks);
+                } else {
+                    commit(&o_full[0]);
+                    if (!two) commit(&o_full[1]);
                 }
                 if (two) {
-                    if (!wait(&p_full[1], pph[1])) break;
-                    pph[1] ^= 1;
-                    tc_fence_after();
-                    sums(1, vs, j == 0);
-                    if (!more) {
-                        if (lane == 0) umma_commit(&o_full[1]);
-                        __syncwarp();
-                    }
+                    if (!sums(1, vs, j == 0)) break;
+                    if (!more) commit(&o_full[1]);
                 }
-                release(vs);
+                commit(&cv_empty[vs]);
                 if (more) {
                     if (two) scores(1, ks);
-                    release(ks);
+                    commit(&cv_empty[ks]);
+                    if (j + 2 == sg.cnt) commit(q_empty);
                 }
             }
         }
-        if (lane == 0) {
+        if (elect_one()) {
             umma_commit(mma_done);
             mbar_wait_drain(mma_done, 0);
         }
         __syncwarp();
-    } else if (warp >= AP_CONV_WARP0 && warp < AP_CONV_WARP0 + 4) {
-        // ---------------- int8 -> fp16 ----------------
+    } else if (warp == AP_Q_WARP) {
+        // ---------------- queries ----------------
+        // rows behind the sequence's last token hold what follows it (or zeros), rows behind the
+        // tile's last token what was there: a row's values go nowhere but its own scores
+        const int tokens = ap_tokens(a.group);
+        uint32_t qph = 0;
+        while (ok && next_seg()) {
+            if (!wait(q_empty, qph ^ 1)) break;
+            qph ^= 1;
+            if (lane == 0) {
+                const int tiles = sg.n > (2 * sg.qt + 1) * tokens ? 2 : 1; // an MMA tile without rows is not used
+                mbar_arrive_expect_tx(q_full, tiles * (D / 64) * tokens * a.group * 128);
+                for (int x = 0; x < tiles; ++x)
+                    for (int i = 0; i < D / 64; ++i)
+                        tma_load_3d(smem_u32(s_q) + x * Q_TILE + i * SLAB, &tm_q, 64 * i, sg.h * a.group,
+                                    sg.q0 + (2 * sg.qt + x) * tokens, q_full);
+            }
+            __syncwarp();
+        }
+        // let the last copies land before the CTA can exit
+        if (qph) mbar_wait_drain(q_full, 0);
+        else mbar_wait_drain(q_full, 1);
+    } else if (warp >= AP_CONV_WARP0) {
+        // ---------------- int8 -> bf16 (K), fp16 (V) ----------------
         const int r = tid - AP_CONV_WARP0 * 32; // row of the tile: a token
         int rs = 0, cs = 0, slot = 0;
         uint32_t rph = 0, cph = 0;
-        bool ok = true;
-        for (int64_t u = u0; u < u1 && ok; u += it.cnt, (u < u1 ? it.next(a, u, u1) : (void)0)) {
-            int unit = AP_NO_UNIT;
-            for (int j = 0; j < it.cnt && ok; ++j) {
+        while (ok && next_seg()) {
+            for (int j = 0; j < sg.cnt && ok; ++j) {
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], rph) && mbar_wait(&cv_empty[cs], cph ^ 1));
-                    if (!ok) break;
-                    int e = 0;
-                    if (kv) {
-                        const float *vs = s_step + slot * 16 + 8;
-                        unit = ap_unit(unit, vs);
-                        e = ap_code_exp(vs[r / AT_GROUP], unit == AP_NO_UNIT ? 0 : unit);
-                    }
-                    // code * 2^e = fma(1152 + code, 2^e, -1152 * 2^e): each a multiple of fp16's
-                    // smallest 2^-24 with few bits, so exact for -24 <= e <= 5
-                    const __half2 mul = __half2half2(__float2half_rn(exp2_int(e)));
-                    const __half2 add = __half2half2(__float2half_rn(-1152.0f * exp2_int(e)));
+                    if (!wait(&raw_full[rs], rph) || !wait(&cv_empty[cs], cph ^ 1)) break;
                     const uint32_t src = smem_u32(s_raw) + rs * R_TILE;
                     unsigned char *dst = s_conv + cs * C_TILE;
+                    // V: code * 2^e = fma(1152 + code, 2^e, -1152 * 2^e), each a multiple of fp16's
+                    // smallest 2^-24 with few bits, so exact for -24 <= e <= 5
+                    const float mf = s_step[slot].mul[r / AT_GROUP];
+                    const __half2 mul = __half2half2(__float2half_rn(mf));
+                    const __half2 add = __half2half2(__float2half_rn(-1152.0f * mf));
+                    uint4 raw[D / 16]; // the whole row: its loads overlap
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) raw[c] = lds128(src + kv_swz<D>(r, c));
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
-                        const uint4 w = lds128(src + kv_swz<D>(r, c));
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
                         uint32_t out[8];
+                        if (kv == 0) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t f = in[i] ^ 0x80808080u;
-                            const uint32_t x = __byte_perm(f, kHalfMagic, 0x4140), y = __byte_perm(f, kHalfMagic, 0x4342);
-                            const __half2 hx = __hfma2(*reinterpret_cast<const __half2 *>(&x), mul, add);
-                            const __half2 hy = __hfma2(*reinterpret_cast<const __half2 *>(&y), mul, add);
-                            out[2 * i] = *reinterpret_cast<const uint32_t *>(&hx);
-                            out[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&hy);
+                            for (int i = 0; i < 4; ++i) codes_to_bf16(in[i], out[2 * i], out[2 * i + 1]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t f = in[i] ^ 0x80808080u;
+                                const uint32_t x = __byte_perm(f, kHalfMagic, 0x4140);
+                                const uint32_t y = __byte_perm(f, kHalfMagic, 0x4342);
+                                const __half2 hx = __hfma2(*reinterpret_cast<const __half2 *>(&x), mul, add);
+                                const __half2 hy = __hfma2(*reinterpret_cast<const __half2 *>(&y), mul, add);
+                                out[2 * i] = *reinterpret_cast<const uint32_t *>(&hx);
+                                out[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&hy);
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -582,176 +782,165 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 slot = (slot + 1) % AP_STEPS;
             }
         }
-    } else if (warp < 8) {
+    } else {
         // ---------------- softmax ----------------
-        const int x = warp >> 2;              // MMA tile
-        const int r = tid & 127;              // row of it = lane of tensor memory
+        const int x = warp >> 3, half = (warp >> 2) & 1; // MMA tile, half of a block's tokens
+        const int r = (warp & 3) * 32 + lane;            // row of the tile = lane of tensor memory
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
-        unsigned char *q_tile = s_q + x * Q_TILE;
-        uint32_t sph = 0, oph = 0;
+        const uint32_t ts = tmem + lanes + x * 128 + half * 64; // this half's scores, then weights
+        const uint32_t to = tmem + lanes + 256 + x * 128 + half * (D / 2);
+        float *mx_mine = s_mx + (x * 2 + half) * 128 + r, *mx_other = s_mx + (x * 2 + (half ^ 1)) * 128 + r;
+        const int tokens = ap_tokens(a.group), rtok = r / a.group, rhead = r - rtok * a.group;
+        uint64_t *pair_bar = pair + x * 4 + (warp & 3);
+        uint32_t sph = 0, oph = 0, turn = 0;
         int slot = 0;
-        bool ok = true;
-        for (int64_t u = u0; u < u1 && ok; u += it.cnt, (u < u1 ? it.next(a, u, u1) : (void)0)) {
-            const int64_t R = (int64_t)it.qt * AP_ROWS + x * 128 + r;
-            const int64_t rows = (int64_t)it.s.n * a.group;
-            const int tok = R < rows ? (int)(R / a.group) : 0;
-            const int head = it.h * a.group + (int)(R - (int64_t)tok * a.group);
-            const bool live = R < rows;
-            const bool used = (int64_t)it.qt * AP_ROWS + x * 128 < rows; // this MMA tile has rows at all
-            const int lim = live ? it.s.len - it.s.n + tok : -1;         // last visible token
-            float fac = 0.0f;
-            {   // queries; the products that read the last ones are complete (their scores were waited for)
-                uint4 w[D / 8];
-                float mx = 0.0f;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + (int64_t)(it.s.q0 + tok) * a.q_stride + (int64_t)(live ? head : 0) * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) w[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx = fmaxf(mx, fmaxf(fabsf(bf16_bits_lo(v[e])), fabsf(bf16_bits_hi(v[e]))));
-                }
-                const float f = half_range_factor(mx);
-                fac = a.scale_log2 / f;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = pack_half2(bf16_bits_lo(v[e]) * f, bf16_bits_hi(v[e]) * f);
-                    *reinterpret_cast<uint4 *>(q_tile + (i >> 3) * SLAB + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[x]);
-            }
-            if (!used) { // keeps step with the issuer
-                slot = (slot + it.cnt) % AP_STEPS;
-                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], oph));
+        auto exchange = [&](float v) { // the same value of the row's other thread
+            mx_mine[turn * 512] = v;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pair_bar);
+            wait(pair_bar, turn);
+            const float o = mx_other[turn * 512];
+            turn ^= 1;
+            return o;
+        };
+        while (ok && next_seg()) {
+            const int tok = (2 * sg.qt + x) * tokens + rtok;
+            const bool live = rtok < tokens && tok < sg.n;
+            if ((2 * sg.qt + x) * tokens >= sg.n) { // a tile without rows keeps step with the issuer
+                slot = (slot + sg.cnt) % AP_STEPS;
+                wait(&o_full[x], oph);
                 oph ^= 1;
                 continue;
             }
+            const int lim = live ? sg.len - sg.n + tok : -1; // last visible token
+            // rows of this warp are consecutive: the first one sees least
+            const int lim_min = __all_sync(0xffffffffu, live) ? __shfl_sync(0xffffffffu, lim, 0) : -1;
             float m = -INFINITY, l = 0.0f;
             int unit = AP_NO_UNIT;
-            // rows of this warp are consecutive: the first one sees least
-            const int lim_min = __shfl_sync(0xffffffffu, lim, 0);
-            const bool ragged = !__all_sync(0xffffffffu, live);
-            for (int j = 0; j < it.cnt; ++j) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], sph));
-                if (!ok) break;
+            for (int j = 0; j < sg.cnt; ++j) {
+                if (!wait(&s_full[x], sph)) break;
                 sph ^= 1;
                 tc_fence_after();
-                const int key0 = (it.j0 + j) * AP_BLOCK;
-                const float *ks = s_step + slot * 16, *vs = ks + 8;
-                const bool masked = ragged || key0 + AP_BLOCK - 1 > lim_min;
+                const ApSteps &st = s_step[slot];
+                const int key0 = (sg.j0 + j) * AP_BLOCK + half * 64;
                 const int vis = lim - key0; // last visible column
-                // the block's largest score
+                const bool masked = key0 + 63 > lim_min;
+                // the largest score
                 float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < AP_BLOCK / 32; ++c) {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
                     uint32_t v[32];
                     tmem_ld32(ts + 32 * c, v);
                     tmem_wait_ld(v);
+                    if (masked) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float best = -INFINITY;
-                        if (masked) {
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i > vis) v[i] = 0xff800000u; // -infinity
+                    }
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (32 * c + 16 * g + i <= vis) best = fmaxf(best, __uint_as_float(v[16 * g + i]));
-                            if (best != -INFINITY) mx = fmaxf(mx, best * (fac * ks[2 * c + g]));
-                        } else {
+                    for (int h = 0; h < 2; ++h) {
+                        float best = __uint_as_float(v[16 * h]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) best = fmaxf(best, __uint_as_float(v[16 * g + i]));
-                            mx = fmaxf(mx, best * (fac * ks[2 * c + g]));
-                        }
+                        for (int i = 1; i < 15; i += 2)
+                            best = max3(best, __uint_as_float(v[16 * h + i]), __uint_as_float(v[16 * h + i + 1]));
+                        best = fmaxf(best, __uint_as_float(v[16 * h + 15]));
+                        mx = fmaxf(mx, best * st.f[4 * half + 2 * c + h]);
                     }
                 }
+                mx = fmaxf(mx, exchange(mx));
                 // the row's reference follows its maximum when it lags too far
                 float al = 1.0f;
-                if (mx > m + AP_LAZY || (m == -INFINITY && mx > m)) {
+                if (mx > m + AP_LAZY) {
                     al = m == -INFINITY ? 0.0f : fast_exp2(m - mx);
                     m = mx;
                     l *= al;
                 }
-                const int unit1 = ap_unit(unit, vs);
-                const bool move = unit1 != unit && unit != AP_NO_UNIT;
-                if (move) al *= exp2_int(unit - unit1);
+                const int unit1 = st.unit;
+                if (unit1 != unit && unit != AP_NO_UNIT) al *= exp2_int(unit - unit1);
                 unit = unit1;
                 if (j > 0 && __any_sync(0xffffffffu, al != 1.0f)) {
                     // scores of this block are complete, so are the sums of the one before
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t v[16];
-                        tmem_ld16(to + 16 * c, v);
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t w[16];
+                        tmem_ld16(to + 16 * c, w);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * al);
-                        tmem_st16(to + 16 * c, v);
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al);
+                        tmem_st16(to + 16 * c, w);
                     }
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
-                const int ub = unit == AP_NO_UNIT ? 0 : unit;
-#pragma unroll
-                for (int c = 0; c < AP_BLOCK / 32; ++c) {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
                     uint32_t v[32], w[16];
                     tmem_ld32(ts + 32 * c, v);
                     tmem_wait_ld(v);
+                    if (masked) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float f = fac * ks[2 * c + g], vg = vs[2 * c + g];
-                        const float rg = vg * exp2_int(-(ub + ap_code_exp(vg, ub)));
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i > vis) v[i] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 4 * half + 2 * c + h;
+                        const float f = st.f[g], off = st.lg[g] - mu;
+                        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            float p0 = fast_exp2(fmaf(__uint_as_float(v[16 * g + i]), f, -mu));
-                            float p1 = fast_exp2(fmaf(__uint_as_float(v[16 * g + i + 1]), f, -mu));
-                            if (masked) {
-                                if (32 * c + 16 * g + i > vis) p0 = 0.0f;
-                                if (32 * c + 16 * g + i + 1 > vis) p1 = 0.0f;
-                            }
-                            l += p0 + p1;
-                            w[8 * g + i / 2] = pack_half2(p0 * rg, p1 * rg);
+                            const float2 t = fma2(make_float2(__uint_as_float(v[16 * h + i]),
+                                                              __uint_as_float(v[16 * h + i + 1])),
+                                                  make_float2(f, f), make_float2(off, off));
+                            const float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                            sum = add2(sum, p);
+                            w[8 * h + i / 2] = pack_half2(p.x, p.y);
                         }
+                        l = fmaf(sum.x + sum.y, st.inv[g], l);
                     }
                     tmem_st16(ts + 16 * c, w); // over scores that have been read
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
+                if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
                 slot = (slot + 1) % AP_STEPS;
             }
             if (!ok) break;
+            l += exchange(l);
             // ---- the tile's sums ----
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], oph));
-            if (!ok) break;
+            if (!wait(&o_full[x], oph)) break;
             oph ^= 1;
             tc_fence_after();
-            const bool whole = it.cnt == it.nkv;
+            const bool whole = sg.cnt == sg.nkv;
             const float us = unit == AP_NO_UNIT ? 0.0f : exp2_int(unit);
-            const float inv = l > 0.0f ? us / l : 0.0f;
-            const int64_t part = (2 * (int64_t)blockIdx.x + (it.j0 == 0 ? 1 : 0)) * AP_ROWS;
-            if (!whole && live) a.part_ml[part + x * 128 + r] = make_float2(m, l);
-            uint16_t *dst = a.out + (int64_t)(it.s.q0 + tok) * a.out_stride + (int64_t)head * D;
-            float4 *pdst = reinterpret_cast<float4 *>(a.part + part * D) + x * 128 + r;
+            const float inv = m > -INFINITY ? us / l : 0.0f;
+            const int64_t part = (2 * (int64_t)blockIdx.x + (sg.j0 == 0 ? 1 : 0)) * AP_ROWS;
+            if (!whole && live && half == 0) a.part_ml[part + x * 128 + r] = make_float2(m, l);
+            const int64_t row_at = live ? (int64_t)(sg.q0 + tok) * a.out_stride +
+                                              ((int64_t)sg.h * a.group + rhead) * D + half * (D / 2)
+                                        : -1;
+            float4 *pdst = reinterpret_cast<float4 *>(a.part + part * D) + (half * (D / 8)) * AP_ROWS + x * 128 + r;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 64; ++c) {
                 uint32_t v[32];
                 tmem_ld32(to + 32 * c, v);
                 tmem_wait_ld(v);
-                if (live && whole) {
+                if (whole) {
+                    // 64 bytes of a row per lane; four lanes turn theirs so that each stores 16 bytes of
+                    // four rows: a store then touches eight lines instead of 32
+                    uint32_t o[4][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t o[4];
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[e] = bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e]) * inv) |
-                                   (bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e + 1]) * inv) << 16);
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+                            o[i][e] = bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e]) * inv) |
+                                      (bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e + 1]) * inv) << 16);
+                    turn4x4(o, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) { // row (lane & ~3) + i, chunk lane & 3
+                        const int64_t at = __shfl_sync(0xffffffffu, row_at, (lane & ~3) + i);
+                        if (at >= 0)
+                            *reinterpret_cast<uint4 *>(a.out + at + 32 * c + 8 * (lane & 3)) =
+                                make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
                     }
                 } else if (live) { // [D / 4][256 rows] groups of four
 #pragma unroll
@@ -776,7 +965,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
 
 // Joins the row tiles that more than one CTA shared and writes zeros for tiles
 // that see nothing.  Tiles are numbered per kv head so that sequence b's start
-// at q_start[b] * group / 256 + b (there is room for each one's tiles).  A thread per
+// at q_start[b] / tokens + b (there is room for each one's tiles).  A thread per
 // row and 16 columns.
 template <int D>
 __global__ void __launch_bounds__(256) k_attention_prompt_join(const AttnArgs a, int ctas)
@@ -789,22 +978,21 @@ __global__ void __launch_bounds__(256) k_attention_prompt_join(const AttnArgs a,
     pdl_wait();
     __syncthreads();
     const int64_t item = blockIdx.x;
+    const int tokens = ap_tokens(a.group), tile = 2 * tokens;
     for (int b = tid; b < a.bt.n_seqs; b += 256) {
         const int64_t lo = a.bt.q_start[b], hi = a.bt.q_start[b + 1];
-        if (lo >= 0 && hi >= lo && hi <= a.bt.T && item >= lo * a.group / AP_ROWS + b &&
-            item < hi * a.group / AP_ROWS + b + 1)
-            s_seq = b;
+        if (lo >= 0 && hi >= lo && hi <= a.bt.T && item >= lo / tile + b && item < hi / tile + b + 1) s_seq = b;
     }
     __syncthreads();
     const int b = s_seq, h = blockIdx.y;
     if (b < 0) return;
     const AttnSeq s = attn_seq(a, b);
-    const int64_t qt64 = item - ((int64_t)s.q0 * a.group / AP_ROWS + b);
+    const int64_t qt64 = item - (s.q0 / tile + b);
     if (s.n == 0 || qt64 >= ap_tiles(s, a.group)) return;
     const int qt = (int)qt64;
     const int nkv = ap_blocks(s, a.group, qt);
     int64_t before = 0;
-    for (int t = tid; t < qt; t += 256) before += ap_blocks(s, a.group, t);
+    for (int t = tid; t < qt; t += 256) before += ap_units(ap_blocks(s, a.group, t));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     if (lane == 0) s_before[warp] = before;
@@ -816,13 +1004,13 @@ __global__ void __launch_bounds__(256) k_attention_prompt_join(const AttnArgs a,
     int c0 = 0, c1 = -1;
     if (nkv > 0) {
         const int64_t active = ap_active(total, ctas);
-        c0 = (int)(((ub + 1) * active - 1) / total);
-        c1 = (int)(((ub + nkv) * active - 1) / total);
+        c0 = (int)(((ub + AP_OVER + 1) * active - 1) / total); // holds the first block
+        c1 = (int)(((ub + AP_OVER + nkv) * active - 1) / total);
         if (c0 == c1) return;
     }
-    const int64_t R = (int64_t)qt * AP_ROWS + tid;
-    if (R >= (int64_t)s.n * a.group) return;
-    const int tok = (int)(R / a.group), g = (int)(R - (int64_t)tok * a.group);
+    const int rtok = (tid & 127) / a.group, g = (tid & 127) - rtok * a.group;
+    const int tok = (2 * qt + (tid >> 7)) * tokens + rtok;
+    if (rtok >= tokens || tok >= s.n) return;
     float m = -INFINITY, l = 0.0f;
     for (int k = c0; k <= c1; ++k)
         m = fmaxf(m, a.part_ml[(2 * (int64_t)k + (k == c0 ? 1 : 0)) * AP_ROWS + tid].x);

@@ -95,6 +95,21 @@ bool encode_codes(CUtensorMap *map, const int8_t *codes, int64_t num_pages, int 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map of the queries: [token][head][D], boxes of 64 elements of one kv head's group and an
+// MMA tile's tokens.
+bool encode_queries(CUtensorMap *map, const void *q, int64_t T, int64_t stride, int n_heads, int group, int d)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n_heads, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)ap_tokens(group)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---- attention: choice of kernel and workspace ----------------------------------
 struct AttnPlan {
     bool ok;
@@ -140,13 +155,15 @@ cudaError_t launch_prompt(const CUtensorMap &tk, const CUtensorMap &tv, const At
 {
     static std::atomic<int> done[kMaxDevices];
     constexpr int smem = ap_smem(D);
+    CUtensorMap tq;
+    if (!encode_queries(&tq, a.q, a.bt.T, a.q_stride, a.kv.hk * a.group, a.group, D)) return cudaErrorInvalidValue;
     cudaError_t e = ensure_smem(k_attention_prompt<D>, smem, done, dev);
     if (e == cudaSuccess) e = launch_pdl(k_attention_plan, dim3(1), dim3(1024), 0, stream, a);
     if (e == cudaSuccess)
-        e = launch_pdl(k_attention_prompt<D>, dim3(ctas), dim3(AP_THREADS), smem, stream, tk, tv, a);
+        e = launch_pdl(k_attention_prompt<D>, dim3(ctas), dim3(AP_THREADS), smem, stream, tk, tv, tq, a);
     if (e == cudaSuccess)
         e = launch_pdl(k_attention_prompt_join<D>,
-                       dim3((unsigned)((int64_t)a.bt.T * a.group / AP_ROWS + a.bt.n_seqs), (unsigned)a.kv.hk, D / 16),
+                       dim3((unsigned)(a.bt.T / (2 * ap_tokens(a.group)) + a.bt.n_seqs), (unsigned)a.kv.hk, D / 16),
                        dim3(256), 0, stream, a, ctas);
     return e;
 }

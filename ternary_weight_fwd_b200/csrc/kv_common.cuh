@@ -15,6 +15,33 @@ __device__ int g_batch_status = 0;
 
 BITNET_DEVINL void record_batch_error() { *(volatile int *)&g_batch_status = BITNET_ERR_INVALID_ARG; }
 
+// Out-of-line part of kv_wait: whether to give up (as mbar_wait does), asked every
+// 256 tries.  t0 = 0 at the first question.
+__device__ __noinline__ bool kv_wait_over(unsigned long long *t0)
+{
+    if (status_failed()) return true;
+    const uint64_t now = globaltimer_ns();
+    if (*t0 == 0) {
+        *t0 = now;
+        return false;
+    }
+    if (now - *t0 <= wait_limit_ns()) return false;
+    record_status(BITNET_ERR_TIMEOUT);
+    return true;
+}
+
+// mbar_wait in few instructions: the kernels below wait at many places, and
+// code beyond the instruction cache costs them more than the waits.
+BITNET_DEVINL bool kv_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint32_t a = smem_u32(bar);
+    unsigned long long t0 = 0;
+    for (uint32_t spin = 1;; ++spin) {
+        if (mbar_try_wait(a, parity)) return true;
+        if ((spin & 255u) == 0 && kv_wait_over(&t0)) return false;
+    }
+}
+
 struct KvView {
     int8_t *k, *v;
     float *k_step, *v_step;

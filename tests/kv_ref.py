@@ -97,7 +97,8 @@ def attention_bound(cache, table, lens, q_start, q, ref, scale=None):
       sum_j (2 2^-11 p_j + min(p_j, 2^-21)) |v_j|, p normalised (the sum is at least the largest weight);
     * a score is a sum of D products of codes (exact in fp16) and queries (bf16, exact in fp16 after scaling),
       in fp32: off by (D + 8) 2^-24 sum_d |q_d k_d| scale at most, which moves p by as much of itself, in the
-      numerator and in the sum; exp2 and the remaining fp32 operations add less than 2^-20 of p each way;
+      numerator and in the sum; exp2 (2.7e-6 of p where a polynomial gives it) and the remaining fp32 operations
+      add less than 2^-18 of p each way;
     * fp32 sums over L tokens: L 2^-24 of sum p |v|, numerator and denominator.
     """
     kc, vc, ks, vs = cache
@@ -123,6 +124,6 @@ def attention_bound(cache, table, lens, q_start, q, ref, scale=None):
                     ds = (kd[:seen] @ np.abs(qq)) * scale * (d + 8) * 2.0 ** -24
                     p = np.exp(s - s.max())
                     p /= p.sum()
-                    rel = 2 * 2.0 ** -11 + 2 * 2.0 ** -20 + 2 * seen * 2.0 ** -24 + 2 * ds.max()
+                    rel = 2 * 2.0 ** -11 + 2 * 2.0 ** -18 + 2 * seen * 2.0 ** -24 + 2 * ds.max()
                     bound[q0 + i, g] = (rel * p + np.minimum(p, 2.0 ** -21)) @ vd[:seen]
     return bound + np.abs(ref) * 2.0 ** -8
