@@ -15,7 +15,7 @@
 // that two or more CTAs share are joined by k_attention_prompt_join through the
 // workspace, in the order of the CTAs.
 //
-// One CTA, 24 warps of 80 registers:
+// One CTA, 24 warps:
 //   warps 0-7, 8-15 softmax of tile A, B: two threads per row, 64 tokens of a block
 //                   each (more warps in flight than a thread per row with 128 scores
 //                   in registers, which was bound by latency).  Weights go back over
@@ -298,6 +298,17 @@ struct ApSeg {
     int pad[3];
 };
 
+template <int N>
+BITNET_DEVINL void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+BITNET_DEVINL void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two fp32 operations in one instruction.
 BITNET_DEVINL float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -461,7 +472,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         return sg.cnt > 0;
     };
 
-    if (warp == AP_SCHED_WARP) {
+    // registers: 16 warps x 88 + 4 x 64 + 4 x 64, the launch's 24 x 80
+    if (warp >= AP_TMA_WARP) {
+      regs_dec<64>();
+      if (warp == AP_SCHED_WARP) {
         // ---------------- tiles ----------------
         const int64_t total = a.base[a.bt.n_seqs];
         const int64_t active = ap_active(total, gridDim.x);
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             if (more) it.next(a);
             if (it.b >= a.bt.n_seqs) it.first = u1;
         }
-    } else if (warp == AP_TMA_WARP) {
+      } else if (warp == AP_TMA_WARP) {
         // ---------------- producer ----------------
         // Lanes 0-7: the 16-token groups of a block.  Page ids are fetched two blocks and
         // steps one block ahead.  A block's steps go to slot (block % 4): its first copy waits
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         }
         for (int s = 0; s < AP_RAW; ++s)
             if (issued & (1u << s)) mbar_wait_drain(&raw_full[s], (last_par >> s) & 1);
-    } else if (warp == AP_MMA_WARP) {
+      } else if (warp == AP_MMA_WARP) {
         // ---------------- MMA issuer ----------------
         // Per block: weights of A times V, next scores of A, then the same for B: while one
         // tile's softmax runs the other's products do.
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             mbar_wait_drain(mma_done, 0);
         }
         __syncwarp();
-    } else if (warp == AP_Q_WARP) {
+      } else {
         // ---------------- queries ----------------
         // rows behind the sequence's last token hold what follows it (or zeros), rows behind the
         // tile's last token what was there: a row's values go nowhere but its own scores
@@ -718,7 +732,9 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         // let the last copies land before the CTA can exit
         if (qph) mbar_wait_drain(q_full, 0);
         else mbar_wait_drain(q_full, 1);
+      }
     } else if (warp >= AP_CONV_WARP0) {
+        regs_dec<64>();
         // ---------------- int8 -> bf16 (K), fp16 (V) ----------------
         const int r = tid - AP_CONV_WARP0 * 32; // row of the tile: a token
         int rs = 0, cs = 0, slot = 0;
@@ -735,12 +751,14 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                     const float mf = s_step[slot].mul[r / AT_GROUP];
                     const __half2 mul = __half2half2(__float2half_rn(mf));
                     const __half2 add = __half2half2(__float2half_rn(-1152.0f * mf));
-                    uint4 raw[D / 16]; // the whole row: its loads overlap
+                    uint4 raw[4]; // loads run four chunks ahead
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) raw[c] = lds128(src + kv_swz<D>(r, c));
+                    for (int c = 0; c < 4; ++c) raw[c] = lds128(src + kv_swz<D>(r, c));
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
-                        const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                        const uint4 now = raw[c & 3];
+                        if (c + 4 < D / 16) raw[c & 3] = lds128(src + kv_swz<D>(r, c + 4));
+                        const uint32_t in[4] = {now.x, now.y, now.z, now.w};
                         uint32_t out[8];
                         if (kv == 0) {
 #pragma unroll
@@ -783,6 +801,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             }
         }
     } else {
+        regs_inc<88>();
         // ---------------- softmax ----------------
         const int x = warp >> 3, half = (warp >> 2) & 1; // MMA tile, half of a block's tokens
         const int r = (warp & 3) * 32 + lane;            // row of the tile = lane of tensor memory
