@@ -25,7 +25,7 @@
 //                   layout that serves K (bf16) as a K-major and V (fp16) as an
 //                   MN-major B operand (a row of V is contiguous in the head
 //                   dimension, the N of that product)
-//   warp 20         TMA of the codes (16-token boxes, one page each); steps
+//   warp 20         TMA of the codes (a box per page); steps
 //   warp 21         MMA issuer, owner of tensor memory
 //   warp 22         queries, as they are (bf16), by TMA
 //   warp 23         walks the unit list and hands out the tiles
@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         // steps one block ahead.  A block's steps go to slot (block % 4): its first copy waits
         // for a raw tile that is free only after the products of the block three before it, so
         // nobody still reads the steps of the block four before.
+        const int page_size = 1 << a.kv.page_shift;
         int j = 0; // of sg
         bool more = next_seg();
         auto fetch = [&](int &page, int &row, bool &valid, bool &head, bool &block) {
@@ -580,7 +581,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             }
             const int ce = max(-24, min(5, step_exp(vs) - unit)); // exponent that goes on the codes
             const float rest = vs > 0.0f ? vs * exp2_int(-(unit + ce)) : 1.0f;
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, valid && page >= 0)) * AT_GROUP * D;
+            const bool copy = valid && page >= 0 && (lane * AT_GROUP & (page_size - 1)) == 0; // a page's first group
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copy)) * page_size * D;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 if (!wait(&raw_empty[stage], phase ^ 1)) break;
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], bytes);
                 __syncwarp();
-                if (valid && page >= 0)
+                if (copy)
                     tma_load_3d(smem_u32(s_raw) + stage * R_TILE + lane * AT_GROUP * D, kv ? &tm_v : &tm_k, 0, row,
                                 page, &raw_full[stage]);
                 issued |= 1u << stage;

@@ -7,23 +7,30 @@
 //
 // Bound by HBM: the codes of K and V are read once (2 D bytes per cached token
 // and kv head; everything else is small).  The work is the list of all
-// (sequence, kv head, chunk of 128 tokens) in that order, cut into equal
-// contiguous shares, one per CTA (one CTA per SM), so ragged batches and single
-// long sequences load every SM alike.  A share's partial softmax of a (sequence,
-// kv head) that it does not hold whole goes to the workspace (at most two per
-// CTA) and k_attention_join adds them up in the order of the CTAs: no atomics,
-// the result does not depend on timing.
+// (sequence, kv head, tile of 8 or 16 rows, chunk of 128 tokens) in that order,
+// cut into equal contiguous shares, one per CTA (one CTA per SM), so ragged
+// batches and single long sequences load every SM alike.  A share's partial
+// softmax of a row tile that it does not hold whole goes to the workspace (at
+// most two per CTA) and k_attention_join adds them up in the order of the CTAs:
+// no atomics, the result does not depend on timing.
 //
 // Within a CTA a producer warp streams chunks through a ring in shared memory by
-// TMA (16-token boxes: one page each, whatever the page size) and eight warps
-// take 16 tokens each, with running maxima and sums of their own, joined once
-// per (sequence, kv head).  The products run on mma.sync m16n8k16 in fp16 with
-// fp32 sums: codes are exact in fp16 (integers up to 128; the byte goes under
-// the exponent of 1024 and 1152 is subtracted), queries are brought into fp16's
-// range by a power of two per row.  K and V fragments are read from the ring in
-// the layout that the bytes already have: an order of the contraction index and
-// of the output columns can be chosen freely, so a lane takes 16 consecutive
-// bytes of a key (K) or of a value (V).
+// TMA, a box per page.  The other warps
+// take the groups of 16 tokens in turn, each with running maxima and sums of its
+// own, joined once per row tile: as many warps as their registers allow (15 for
+// tiles of 8 rows, 11 for 16), since one warp's chain of loads, products and
+// exponentials leaves most of its time unused.
+// The products run on mma.sync m16n8k16 in fp16 with fp32 sums and the tokens
+// (K) and the head dimension (V transposed) on the side of 16, the rows on the
+// side of 8: a row tile needs half the instructions and registers that it would
+// with its rows on the side of 16, and what costs here is instructions per byte
+// of codes (rows on 16 with eight warps: 51 us for one sequence of 131071 tokens,
+// 3.3 TB/s).  Codes are exact in fp16 (the byte goes under the exponent of 1024
+// and 1152 is subtracted), queries are brought into fp16's range by a power of two
+// per row.  K and V fragments are read from the ring in the layout that the bytes
+// already have: an order of the contraction index and of the output rows can be
+// chosen freely, so a lane takes 16 consecutive bytes of a key (K) or of a value
+// (V).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -33,13 +40,13 @@
 namespace bitnet {
 
 constexpr int AT_CHUNK = 128;   // tokens per ring stage
-constexpr int AT_GROUP = 16;    // tokens per warp and stage, and per TMA box
-constexpr int AT_WARPS = 8;     // consumer warps
-constexpr int AT_THREADS = (AT_WARPS + 1) * 32;
+constexpr int AT_GROUP = 16;    // tokens a warp takes at a time (a page holds at least as many)
+constexpr int AT_GROUPS = AT_CHUNK / AT_GROUP;
 constexpr int AT_STAGES = 5;
 constexpr int AT_MAX_ROWS = 32; // query rows per (sequence, kv head)
 constexpr int AT_MAX_CTAS = 160;
 constexpr int AT_MIN_UNITS = 2; // chunks worth a CTA of their own
+constexpr float AT_LAZY = 8.0f; // a row's exponents refer to a maximum up to 2^8 behind
 
 struct AttnArgs {
     KvView kv;
@@ -56,10 +63,13 @@ struct AttnArgs {
     int64_t *base;     // [n_seqs + 1] first unit of each sequence
 };
 
-constexpr __host__ __device__ int at_smem(int d, int mt)
+// Consumer warps for nq tiles of 8 rows; with the producer they fill 16 (12) warps of 128 (168) registers.
+constexpr __host__ __device__ int at_warps(int nq) { return nq == 1 ? 15 : 11; }
+
+constexpr __host__ __device__ int at_smem(int d, int nq)
 {
-    return 1024 + AT_STAGES * 2 * AT_CHUNK * d + 16 * mt * (2 * d + 16) + AT_WARPS * 16 * mt * (36 * 4 + 8) +
-           16 * mt * 8 + 1024;
+    return 1024 + AT_STAGES * 2 * AT_CHUNK * d + 8 * nq * (2 * d + 16) + at_warps(nq) * 8 * nq * (36 * 4 + 8) +
+           8 * nq * 8 + 1024;
 }
 
 // 3-D tiled tensor copy global -> shared (no multicast); c0 is 0 here.
@@ -115,6 +125,14 @@ BITNET_DEVINL uint32_t pack_half2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// Transposes an 8 x 8 tile of fp16 held as row = lane / 4, columns 2 (lane % 4), + 1.
+BITNET_DEVINL uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 BITNET_DEVINL float fast_exp2(float x)
 {
     float y;
@@ -167,20 +185,34 @@ BITNET_DEVINL int64_t attn_active(int64_t units, int ctas)
     return want < ctas ? want : ctas;
 }
 
+// Row tiles of `rows` rows per kv head of a sequence, and its units.
+BITNET_DEVINL int attn_row_tiles(const AttnArgs &a, const AttnSeq &s, int rows) { return (s.n * a.group + rows - 1) / rows; }
+BITNET_DEVINL int64_t attn_units(const AttnArgs &a, const AttnSeq &s, int rows)
+{
+    return (int64_t)a.kv.hk * attn_row_tiles(a, s, rows) * attn_chunks(s);
+}
+
 // Walks the unit list: sequence of unit u, given a sequence at or before it.
 struct UnitIter {
     int b;
     int64_t base; // first unit of sequence b
     AttnSeq s;
-    int nc;       // chunks per kv head
+    int nc, nt;   // chunks, row tiles per kv head
 
-    BITNET_DEVINL void seek(const AttnArgs &a, int64_t u)
+    BITNET_DEVINL void load(const AttnArgs &a, int rows)
     {
-        while (u >= base + (int64_t)nc * a.kv.hk && b + 1 < a.bt.n_seqs) {
-            base += (int64_t)nc * a.kv.hk;
+        s = attn_seq(a, b);
+        nc = attn_chunks(s);
+        nt = attn_row_tiles(a, s, rows);
+    }
+    BITNET_DEVINL void seek(const AttnArgs &a, int64_t u, int rows)
+    {
+        for (;;) {
+            const int64_t n = (int64_t)a.kv.hk * nt * nc;
+            if (u < base + n || b + 1 >= a.bt.n_seqs) return;
+            base += n;
             ++b;
-            s = attn_seq(a, b);
-            nc = attn_chunks(s);
+            load(a, rows);
         }
     }
 };
@@ -193,13 +225,15 @@ BITNET_DEVINL uint32_t kv_swz(int r, int c)
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(AT_THREADS, 1)
+// NQ: tiles of 8 query rows.
+template <int D, int NQ>
+__global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
     k_attention_tokens(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const AttnArgs a)
 {
-    constexpr int NT = D / 8;               // output column tiles
-    constexpr int ROWS = 16 * MT;
+    constexpr int WARPS = at_warps(NQ), THREADS = (WARPS + 1) * 32;
+    constexpr int DT = D / 16;              // output tiles of 16 elements
+    constexpr int ROWS = 8 * NQ;
     constexpr uint32_t TILE = AT_CHUNK * D; // bytes of K (or V) per stage
     constexpr int QROW = 2 * D + 16;        // bytes of a query row in shared memory
     constexpr int MROW = 36;                // floats of a row of the join buffer
@@ -209,26 +243,26 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     uint64_t *empty = full + AT_STAGES;
-    int64_t *s_u = reinterpret_cast<int64_t *>(empty + AT_STAGES); // total units, first sequence's base
-    int *s_b = reinterpret_cast<int *>(s_u + 2);
-    float *s_step = reinterpret_cast<float *>(s_b + 4); // [stages][2][8]
-    int64_t *s_scan = reinterpret_cast<int64_t *>(smem + 640); // [9] warp sums
+    int64_t *s_u = reinterpret_cast<int64_t *>(empty + AT_STAGES); // first sequence's base
+    int *s_b = reinterpret_cast<int *>(s_u + 1);
+    float *s_step = reinterpret_cast<float *>(smem + 128);        // [stages][2][8]
+    int64_t *s_scan = reinterpret_cast<int64_t *>(smem + 640);    // [WARPS + 1] warp sums
     unsigned char *ring = smem + 1024;
     unsigned char *s_q = ring + AT_STAGES * 2 * TILE;
-    float *s_join = reinterpret_cast<float *>(s_q + ROWS * QROW);       // [8 warps][ROWS][36]
-    float2 *s_ml = reinterpret_cast<float2 *>(s_join + AT_WARPS * ROWS * MROW); // [8][ROWS]
-    float *s_fac = reinterpret_cast<float *>(s_ml + AT_WARPS * ROWS);   // [ROWS] score factor
-    int *s_lim = reinterpret_cast<int *>(s_fac + ROWS);                 // [ROWS] last visible position
+    float *s_join = reinterpret_cast<float *>(s_q + ROWS * QROW);               // [WARPS][ROWS][36]
+    float2 *s_ml = reinterpret_cast<float2 *>(s_join + WARPS * ROWS * MROW);    // [WARPS][ROWS]
+    float *s_fac = reinterpret_cast<float *>(s_ml + WARPS * ROWS);              // [ROWS] score factor
+    int *s_lim = reinterpret_cast<int *>(s_fac + ROWS);                         // [ROWS] last visible position
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < AT_STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], AT_WARPS);
+            mbar_init(&empty[s], AT_GROUPS); // one arrival per group, by the warp that took it
         }
         fence_mbarrier_init();
     }
-    if (tid == AT_WARPS * 32) {
+    if (tid == WARPS * 32) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
@@ -236,10 +270,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     pdl_wait();
 
     // ---- total units, this CTA's share and the sequence it starts in ----
-    const int per = (a.bt.n_seqs + AT_THREADS - 1) / AT_THREADS;
+    const int per = (a.bt.n_seqs + THREADS - 1) / THREADS;
     const int b_lo = min(a.bt.n_seqs, tid * per), b_hi = min(a.bt.n_seqs, b_lo + per);
     int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += (int64_t)attn_chunks(attn_seq(a, b)) * a.kv.hk;
+    for (int b = b_lo; b < b_hi; ++b) mine += attn_units(a, attn_seq(a, b), ROWS);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -250,7 +284,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     __syncthreads();
     int64_t before = incl - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w <= AT_WARPS; ++w) {
+    for (int w = 0; w <= WARPS; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
@@ -261,7 +295,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         int64_t at = before;
         for (int b = b_lo; b < b_hi; ++b) {
             a.base[b] = at;
-            at += (int64_t)attn_chunks(attn_seq(a, b)) * a.kv.hk;
+            at += attn_units(a, attn_seq(a, b), ROWS);
         }
         if (tid == 0) a.base[a.bt.n_seqs] = total;
     }
@@ -269,7 +303,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     if (u0 >= before && u0 < before + mine) {
         int64_t at = before;
         for (int b = b_lo; b < b_hi; ++b) {
-            const int64_t un = (int64_t)attn_chunks(attn_seq(a, b)) * a.kv.hk;
+            const int64_t un = attn_units(a, attn_seq(a, b), ROWS);
             if (u0 < at + un) {
                 s_b[0] = b;
                 s_u[0] = at;
@@ -282,14 +316,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     UnitIter it;
     it.b = s_b[0];
     it.base = s_u[0];
-    it.s = attn_seq(a, it.b);
-    it.nc = attn_chunks(it.s);
+    it.load(a, ROWS);
 
-    if (warp == AT_WARPS) {
+    if (warp == WARPS) {
         // ---------------- producer ----------------
         // A batch of four chunks: lane = chunk * 8 + 16-token group.  Page ids are
         // fetched two batches ahead and steps one batch ahead of their copies.
-        const int sub = lane >> 3, grp = lane & 7;
+        const int sub = lane >> 3, grp = lane & 7, page_size = 1 << a.kv.page_shift;
         int page1 = -1, row1 = 0; // next batch
         bool valid1 = false;
         auto fetch = [&](int64_t u, int &page, int &row, bool &valid) {
@@ -297,13 +330,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             page = -1;
             row = 0;
             if (u < u1) {
-                it.seek(a, u);
+                it.seek(a, u, ROWS);
                 const int rel = (int)(u - it.base);
-                const int h = rel / it.nc, key0 = (rel - h * it.nc) * AT_CHUNK + grp * AT_GROUP;
+                const int ht = rel / it.nc, key0 = (rel - ht * it.nc) * AT_CHUNK + grp * AT_GROUP;
                 if (key0 < it.s.len) {
                     valid = true;
                     page = page_of(a.kv, a.bt, it.b, key0 >> a.kv.page_shift);
-                    row = (h << a.kv.page_shift) + (key0 & ((1 << a.kv.page_shift) - 1));
+                    row = ((ht / it.nt) << a.kv.page_shift) + (key0 & ((1 << a.kv.page_shift) - 1));
                 }
             }
         };
@@ -331,18 +364,19 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             fetch(u + 8 + sub, page2, row2, valid2);
 #pragma unroll 1
             for (int s = 0; s < 4 && u + s < u1; ++s) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1));
+                ok = __all_sync(0xffffffffu, kv_wait(&empty[stage], phase ^ 1));
                 if (!ok) break;
                 const bool here = sub == s && valid;
                 if (here) {
                     s_step[stage * 16 + grp] = ks;
                     s_step[stage * 16 + 8 + grp] = vs;
                 }
-                const int copies = __popc(__ballot_sync(0xffffffffu, here && page >= 0));
+                const bool copy = here && page >= 0 && (grp * AT_GROUP & (page_size - 1)) == 0; // a page's first group
+                const int copies = __popc(__ballot_sync(0xffffffffu, copy));
                 __syncwarp(); // the steps are written before the arrival that shows them
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], copies * 2 * AT_GROUP * D);
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], copies * 2 * page_size * D);
                 __syncwarp();
-                if (here && page >= 0) {
+                if (copy) {
                     const uint32_t dst = smem_u32(ring) + stage * 2 * TILE + grp * AT_GROUP * D;
                     tma_load_3d(dst, &tm_k, 0, row, page, &full[stage]);
                     tma_load_3d(dst + TILE, &tm_v, 0, row, page, &full[stage]);
@@ -371,30 +405,31 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 
     // ---------------- consumers ----------------
     const int g = lane >> 2, c = lane & 3;
-    const int perm_g = (g & 1) ? ((g + 4) & 7) : g; // token of MMA column g: 0 5 2 7 4 1 6 3 (see below)
-    const int key_e = 2 * c, key_o = (2 * c + 5) & 7; // tokens of this lane's two score columns
+    const int key_g = (g & 1) ? ((g + 4) & 7) : g;      // token of score row g (g + 8: + 8): 0 5 2 7 4 1 6 3, see below
+    const int key_e = 2 * c, key_o = (2 * c + 5) & 7;   // tokens of contraction indices 2c, 2c + 1 of the second product
     const uint32_t q_base = smem_u32(s_q), ring_base = smem_u32(ring);
-    int stage = 0;
-    uint32_t phase = 0;
+    int n = warp; // this warp's next group, counted from the CTA's first chunk
     bool ok = true;
+    auto sync_consumers = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
 
     for (int64_t u = u0; u < u1;) {
-        it.seek(a, u);
+        it.seek(a, u, ROWS);
         const int rel = (int)(u - it.base);
-        const int h = rel / it.nc, t0 = rel - h * it.nc;
+        const int ht = rel / it.nc, t0 = rel - ht * it.nc;
+        const int h = ht / it.nt, r0 = (ht - h * it.nt) * ROWS; // kv head, first row of the tile
         const int cnt = (int)min((int64_t)(it.nc - t0), u1 - u);
-        const int nrow = it.s.n * a.group; // <= ROWS by the host's choice of MT and the check of n
+        const int nrow = min(ROWS, it.s.n * a.group - r0);
         const int len = it.s.len, first = len - it.s.n;
 
-        // queries of this (sequence, kv head), scaled into fp16's range row by row
-        for (int r = warp; r < ROWS; r += AT_WARPS) {
+        // queries of this row tile, scaled into fp16's range row by row
+        for (int r = warp; r < ROWS; r += WARPS) {
             float x[D / 32];
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
-            const int tok = r / a.group;
+            const int tok = (r0 + r) / a.group;
             if (r < nrow) {
                 const uint16_t *p = a.q + (int64_t)(it.s.q0 + tok) * a.q_stride +
-                                    ((int64_t)h * a.group + (r - tok * a.group)) * D + lane * (D / 32);
+                                    ((int64_t)h * a.group + (r0 + r - tok * a.group)) * D + lane * (D / 32);
                 if constexpr (D == 128) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(p);
                     x[0] = bf16_bits_lo(w.x);
@@ -420,100 +455,111 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                 s_lim[r] = r < nrow ? first + tok : -1;
             }
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(AT_WARPS * 32) : "memory");
+        sync_consumers();
 
-        float o[MT][NT][4], m[MT][2], l[MT][2], fac[MT][2];
-        int lim[MT][2];
+        // rows of this lane: 8 t + 2 c and + 1 (scores and weights), 8 t + g (queries)
+        uint32_t qb[NQ][D / 64][8]; // contraction step 4 hh + w: qb[t][hh][2 w], [2 w + 1]
+        float o[NQ][DT][4], m[NQ][2], l[NQ][2], fac[NQ][2];
+        int lim[NQ][2];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < NQ; ++t) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
+            for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 w = lds128(q_base + (8 * t + g) * QROW + (c + 4 * hh) * 32 + 16 * e);
+                    qb[t][hh][4 * e] = w.x;
+                    qb[t][hh][4 * e + 1] = w.y;
+                    qb[t][hh][4 * e + 2] = w.z;
+                    qb[t][hh][4 * e + 3] = w.w;
+                }
+#pragma unroll
+            for (int n = 0; n < DT; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m[t][e] = -INFINITY;
                 l[t][e] = 0.0f;
-                fac[t][e] = s_fac[16 * t + 8 * e + g];
-                lim[t][e] = s_lim[16 * t + 8 * e + g];
+                fac[t][e] = s_fac[8 * t + 2 * c + e];
+                lim[t][e] = s_lim[8 * t + 2 * c + e];
             }
         }
         float unit = 0.0f, inv_unit = 0.0f; // o is in units of this power of two; 0: not chosen yet
 
-        for (int i = 0; i < cnt; ++i) {
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(&full[stage], phase));
-            const int key0 = (t0 + i) * AT_CHUNK + warp * AT_GROUP;
+        const int n_end = (int)(u - u0 + cnt) * AT_GROUPS;
+        for (; n < n_end; n += WARPS) {
+            const int chunk = n / AT_GROUPS;
+            const int member = (int)(n % AT_GROUPS), st = (int)(chunk % AT_STAGES);
+            ok = __all_sync(0xffffffffu, ok && kv_wait(&full[st], (uint32_t)(chunk / AT_STAGES) & 1u));
+            const int key0 = (t0 + chunk - (int)(u - u0)) * AT_CHUNK + member * AT_GROUP;
             if (ok && key0 < len) {
-                const float ks = s_step[stage * 16 + warp], vs = s_step[stage * 16 + 8 + warp];
-                const uint32_t kb = ring_base + stage * 2 * TILE + warp * AT_GROUP * D, vb = kb + TILE;
-                float s[MT][2][4];
+                const float ks = s_step[st * 16 + member], vs = s_step[st * 16 + 8 + member];
+                const uint32_t kb = ring_base + st * 2 * TILE + member * AT_GROUP * D, vb = kb + TILE;
+                float s[NQ][4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.0f;
-                // scores.  Contraction step 4 hh + w takes elements 16 (c + 4 hh) + 4 w .. + 3 of
-                // lane column c.  Column g of MMA j is token 8 j + perm(g): the two tokens of a
+                for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+                // scores: tokens x rows.  Contraction step 4 hh + w takes elements 16 (c + 4 hh) + 4 w
+                // .. + 3 of lane column c.  Score row g is token key_g: the two tokens of a
                 // shared-memory wavefront differ in bit 2, so their swizzled chunks differ.
 #pragma unroll
                 for (int hh = 0; hh < D / 64; ++hh) {
-                    uint4 kw[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) kw[j] = lds128(kb + kv_swz<D>(8 * j + perm_g, c + 4 * hh));
-                    uint4 qa[MT][4]; // rows g and g + 8, 16 elements each
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t qp = q_base + (16 * t + 8 * e + g) * QROW + (c + 4 * hh) * 32;
-                            qa[t][2 * e] = lds128(qp);
-                            qa[t][2 * e + 1] = lds128(qp + 16);
-                        }
+                    const uint4 k0 = lds128(kb + kv_swz<D>(key_g, c + 4 * hh));
+                    const uint4 k1 = lds128(kb + kv_swz<D>(8 + key_g, c + 4 * hh));
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        uint32_t b0[2], b1[2];
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_half(w0[w] ^ 0x80808080u, a0, a2);
+                        codes_to_half(w1[w] ^ 0x80808080u, a1, a3);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t word = w == 0 ? kw[j].x : w == 1 ? kw[j].y : w == 2 ? kw[j].z : kw[j].w;
-                            codes_to_half(word ^ 0x80808080u, b0[j], b1[j]);
-                        }
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            const uint4 lo = qa[t][w >> 1], hi = qa[t][2 + (w >> 1)];
-                            const uint32_t a0 = (w & 1) ? lo.z : lo.x, a2 = (w & 1) ? lo.w : lo.y;
-                            const uint32_t a1 = (w & 1) ? hi.z : hi.x, a3 = (w & 1) ? hi.w : hi.y;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) mma_f16(s[t][j], a0, a1, a2, a3, b0[j], b1[j]);
-                        }
+                        for (int t = 0; t < NQ; ++t)
+                            mma_f16(s[t], a0, a1, a2, a3, qb[t][hh][2 * w], qb[t][hh][2 * w + 1]);
                     }
                 }
-                // softmax: lane holds rows g, g + 8 x tokens key_e, key_o, 8 + key_e, 8 + key_o
+                // the values' codes are on their way during the softmax
+                uint32_t vw[4][D / 32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rw = (k & 1 ? key_o : key_e) + 8 * (k >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 w = lds128(vb + kv_swz<D>(rw, g));
+                        vw[k][0] = w.x;
+                        vw[k][1] = w.y;
+                        vw[k][2] = w.z;
+                        vw[k][3] = w.w;
+                    } else {
+                        const uint2 w = lds64(vb + kv_swz<D>(rw, g >> 1) + 8 * (g & 1));
+                        vw[k][0] = w.x;
+                        vw[k][1] = w.y;
+                    }
+                }
+                // softmax: s[t][2 k + e] is token key_g + 8 k, row 8 t + 2 c + e
                 const bool masked = key0 + AT_GROUP - 1 > first;
                 bool grown = false;
-                float mx[MT][2];
+                float mx[NQ][2];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int t = 0; t < NQ; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float f = fac[t][e] * ks;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float &x0 = s[t][j][2 * e], &x1 = s[t][j][2 * e + 1];
-                            x0 *= f;
-                            x1 *= f;
-                            if (masked) {
-                                if (key0 + 8 * j + key_e > lim[t][e]) x0 = -INFINITY;
-                                if (key0 + 8 * j + key_o > lim[t][e]) x1 = -INFINITY;
-                            }
+                        float &x0 = s[t][e], &x1 = s[t][2 + e];
+                        x0 *= f;
+                        x1 *= f;
+                        if (masked) {
+                            if (key0 + key_g > lim[t][e]) x0 = -INFINITY;
+                            if (key0 + 8 + key_g > lim[t][e]) x1 = -INFINITY;
                         }
-                        float v = fmaxf(fmaxf(s[t][0][2 * e], s[t][0][2 * e + 1]),
-                                        fmaxf(s[t][1][2 * e], s[t][1][2 * e + 1]));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                        mx[t][e] = fmaxf(v, m[t][e]);
-                        grown |= mx[t][e] > m[t][e];
+                        float v = fmaxf(x0, x1);
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        mx[t][e] = v;
+                        grown |= v > m[t][e] + AT_LAZY;
                     }
-                // o follows the running maximum, and keeps units near the current page's v_step
-                // (weights times v_step / unit stay in fp16's range whatever the steps of other pages)
+                // a row's reference follows its maximum when it lags too far, and o keeps units near the
+                // current page's v_step: weights times v_step / unit stay in fp16's range, whatever the
+                // steps of other pages
                 float r = vs * inv_unit;
-                const bool move = vs > 0.0f && !(r >= 0x1p-4f && r <= 0x1p8f);
+                const bool move = vs > 0.0f && !(r >= 0x1p-4f && r <= 0x1p4f);
                 if (__any_sync(0xffffffffu, grown) || move) {
                     float us = 1.0f;
                     if (move) {
@@ -524,135 +570,113 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                         r = vs * inv_unit;
                     }
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
+                    for (int t = 0; t < NQ; ++t)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float al = mx[t][e] > m[t][e] ? fast_exp2(m[t][e] - mx[t][e]) : 1.0f;
-                            m[t][e] = mx[t][e];
-                            l[t][e] *= al;
+                            float al = 1.0f;
+                            if (mx[t][e] > m[t][e] + AT_LAZY) {
+                                al = fast_exp2(m[t][e] - mx[t][e]);
+                                m[t][e] = mx[t][e];
+                                l[t][e] *= al;
+                            }
                             const float ou = al * us;
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                o[t][n][2 * e] *= ou;
-                                o[t][n][2 * e + 1] *= ou;
+                            for (int n = 0; n < DT; ++n) {
+                                o[t][n][e] *= ou;
+                                o[t][n][2 + e] *= ou;
                             }
                         }
                 }
-                uint32_t pa[MT][4];
+                uint32_t pb[NQ][2];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int t = 0; t < NQ; ++t) {
+                    float p[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float mu = m[t][e] == -INFINITY ? 0.0f : m[t][e];
-                        float p[4];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            p[2 * j] = fast_exp2(s[t][j][2 * e] - mu);
-                            p[2 * j + 1] = fast_exp2(s[t][j][2 * e + 1] - mu);
-                        }
-                        l[t][e] += (p[0] + p[1]) + (p[2] + p[3]);
-                        pa[t][e] = pack_half2(p[0] * r, p[1] * r);
-                        pa[t][2 + e] = pack_half2(p[2] * r, p[3] * r);
+                        p[e] = fast_exp2(s[t][e] - mu);
+                        p[2 + e] = fast_exp2(s[t][2 + e] - mu);
+                        l[t][e] += p[e] + p[2 + e];
                     }
-                // o += p v.  Lane column g of output tile n is element (D / 8) g + n; contraction
-                // indices 2c, 2c + 1 (+ 8) are tokens key_e, key_o (+ 8).
+                    pb[t][0] = transpose8(pack_half2(p[0] * r, p[1] * r));
+                    pb[t][1] = transpose8(pack_half2(p[2] * r, p[3] * r));
+                }
+                // o += v^T p: elements x rows.  Output rows g, g + 8 of tile n are elements
+                // (D / 8) g + 2 n, + 1; contraction indices 2c, 2c + 1 (+ 8) are tokens key_e, key_o (+ 8).
                 if (vs > 0.0f) {
-                    uint32_t vw[4][D / 32];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int rw = (k & 1 ? key_o : key_e) + 8 * (k >> 1);
-                        if constexpr (D == 128) {
-                            const uint4 w = lds128(vb + kv_swz<D>(rw, g));
-                            vw[k][0] = w.x;
-                            vw[k][1] = w.y;
-                            vw[k][2] = w.z;
-                            vw[k][3] = w.w;
-                        } else {
-                            const uint2 w = lds64(vb + kv_swz<D>(rw, g >> 1) + 8 * (g & 1));
-                            vw[k][0] = w.x;
-                            vw[k][1] = w.y;
-                        }
-                    }
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w) {
-                        uint32_t bb[2][4]; // [b0, b1][tile 4 w + x]
+                        uint32_t ab[2][4]; // [tokens 0-7, 8-15][element 4 w + x]
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const uint32_t x = vw[2 * e][w] ^ 0x80808080u, y = vw[2 * e + 1][w] ^ 0x80808080u;
-                            codes_to_half(__byte_perm(x, y, 0x5140), bb[e][0], bb[e][1]);
-                            codes_to_half(__byte_perm(x, y, 0x7362), bb[e][2], bb[e][3]);
+                            codes_to_half(__byte_perm(x, y, 0x5140), ab[e][0], ab[e][1]);
+                            codes_to_half(__byte_perm(x, y, 0x7362), ab[e][2], ab[e][3]);
                         }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                            for (int t = 0; t < MT; ++t)
-                                mma_f16(o[t][4 * w + x], pa[t][0], pa[t][1], pa[t][2], pa[t][3], bb[0][x], bb[1][x]);
+                            for (int t = 0; t < NQ; ++t)
+                                mma_f16(o[t][2 * w + x], ab[0][2 * x], ab[0][2 * x + 1], ab[1][2 * x], ab[1][2 * x + 1],
+                                        pb[t][0], pb[t][1]);
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (++stage == AT_STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
+            if (lane == 0) mbar_arrive(&empty[st]);
         }
 
-        // ---- join the eight warps ----
+        // ---- join the warps ----
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < NQ; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 1);
-                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 2);
-                if (c == 0) s_ml[warp * ROWS + 16 * t + 8 * e + g] = make_float2(m[t][e], l[t][e]);
-            }
-        asm volatile("bar.sync 1, %0;" ::"n"(AT_WARPS * 32) : "memory");
-        float wf[MT][2]; // this warp's weight of rows g, g + 8
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+                for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
+                if (g == 0) s_ml[warp * ROWS + 8 * t + 2 * c + e] = make_float2(m[t][e], l[t][e]);
+            }
+        sync_consumers();
+        float wf[NQ][2]; // this warp's weight of its rows
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float mm = -INFINITY;
-                for (int w = 0; w < AT_WARPS; ++w) mm = fmaxf(mm, s_ml[w * ROWS + 16 * t + 8 * e + g].x);
+                for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_ml[w * ROWS + 8 * t + 2 * c + e].x);
                 wf[t][e] = m[t][e] == -INFINITY ? 0.0f : fast_exp2(m[t][e] - mm) * unit;
             }
         const bool whole = cnt == it.nc;
         const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-        // thread -> (row, column tile) of the result
+        // thread -> (row, eighth of the head dimension) of the result
         const int jr = tid >> 3, jn = tid & 7;
         float jm = -INFINITY, jl = 0.0f;
-        if (jr < ROWS && jr < nrow) {
-            for (int w = 0; w < AT_WARPS; ++w) jm = fmaxf(jm, s_ml[w * ROWS + jr].x);
+        if (jr < nrow) {
+            for (int w = 0; w < WARPS; ++w) jm = fmaxf(jm, s_ml[w * ROWS + jr].x);
             if (jm != -INFINITY)
-                for (int w = 0; w < AT_WARPS; ++w) {
+                for (int w = 0; w < WARPS; ++w) {
                     const float2 x = s_ml[w * ROWS + jr];
                     jl += x.y * fast_exp2(x.x - jm);
                 }
             if (!whole && jn == 0) a.part_ml[(int64_t)slot * ROWS + jr] = make_float2(jm, jl);
         }
         const float inv = jl > 0.0f ? 1.0f / jl : 0.0f;
-        const int jtok = jr / a.group;
+        const int jtok = (r0 + jr) / a.group;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            if (w) asm volatile("bar.sync 1, %0;" ::"n"(AT_WARPS * 32) : "memory");
+            if (w) sync_consumers();
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
+            for (int t = 0; t < NQ; ++t)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (16 * t + 8 * e + g >= nrow) continue;
-                    float *dst = s_join + (warp * ROWS + 16 * t + 8 * e + g) * MROW;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<float4 *>(dst + (2 * c + k) * 4) =
-                            make_float4(o[t][4 * w][2 * e + k] * wf[t][e], o[t][4 * w + 1][2 * e + k] * wf[t][e],
-                                        o[t][4 * w + 2][2 * e + k] * wf[t][e], o[t][4 * w + 3][2 * e + k] * wf[t][e]);
-                }
-            asm volatile("bar.sync 1, %0;" ::"n"(AT_WARPS * 32) : "memory");
-            if (jr < ROWS && jr < nrow) {
+                for (int e = 0; e < 2; ++e)
+                    if (8 * t + 2 * c + e < nrow)
+                        *reinterpret_cast<float4 *>(s_join + (warp * ROWS + 8 * t + 2 * c + e) * MROW + g * 4) =
+                            make_float4(o[t][2 * w][e] * wf[t][e], o[t][2 * w][2 + e] * wf[t][e],
+                                        o[t][2 * w + 1][e] * wf[t][e], o[t][2 * w + 1][2 + e] * wf[t][e]);
+            sync_consumers();
+            if (jr < nrow) {
                 float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int k = 0; k < AT_WARPS; ++k) {
+                for (int k = 0; k < WARPS; ++k) {
                     const float4 y = *reinterpret_cast<const float4 *>(s_join + (k * ROWS + jr) * MROW + jn * 4);
                     x.x += y.x;
                     x.y += y.y;
@@ -662,7 +686,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                 const int d = (D / 8) * jn + 4 * w;
                 if (whole) {
                     uint16_t *p = a.out + (int64_t)(it.s.q0 + jtok) * a.out_stride +
-                                  ((int64_t)h * a.group + (jr - jtok * a.group)) * D + d;
+                                  ((int64_t)h * a.group + (r0 + jr - jtok * a.group)) * D + d;
                     *reinterpret_cast<uint2 *>(p) =
                         make_uint2(bf16_rn_bits(x.x * inv) | (bf16_rn_bits(x.y * inv) << 16),
                                    bf16_rn_bits(x.z * inv) | (bf16_rn_bits(x.w * inv) << 16));
@@ -677,7 +701,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
 }
 
-// Joins the parts of every (sequence, kv head) that more than one CTA shared,
+// Joins the parts of every row tile (of `rows` rows) that more than one CTA shared,
 // and writes zeros for rows of sequences without cached tokens.  A warp per row;
 // parts are added in the order of the CTAs.
 template <int D>
@@ -701,12 +725,12 @@ __global__ void __launch_bounds__(128) k_attention_join(const AttnArgs a, int ro
     float inv = 0.0f;
     if (nc > 0) {
         const int64_t active = attn_active(total, ctas);
-        const int64_t ub = base + (int64_t)h * nc, ue = ub + nc - 1;
+        const int64_t ub = base + ((int64_t)h * attn_row_tiles(a, s, rows) + r / rows) * nc, ue = ub + nc - 1;
         const int c0 = (int)(((ub + 1) * active - 1) / total), c1 = (int)(((ue + 1) * active - 1) / total);
         if (c0 == c1) return; // one CTA held it whole and wrote the result
         float m = -INFINITY;
         for (int k = c0 + lane; k <= c1; k += 32)
-            m = fmaxf(m, a.part_ml[(int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r].x);
+            m = fmaxf(m, a.part_ml[(int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r % rows].x);
         m = warp_max(m);
         if (m != -INFINITY) {
             float l = 0.0f;
@@ -714,7 +738,7 @@ __global__ void __launch_bounds__(128) k_attention_join(const AttnArgs a, int ro
                 const int k = k0 + lane;
                 float f = 0.0f;
                 if (k <= c1) {
-                    const float2 ml = a.part_ml[(int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r];
+                    const float2 ml = a.part_ml[(int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r % rows];
                     f = fast_exp2(ml.x - m);
                     l += ml.y * f;
                 }
@@ -722,7 +746,7 @@ __global__ void __launch_bounds__(128) k_attention_join(const AttnArgs a, int ro
                 for (int i = 0; i < cnt; ++i) {
                     const float fi = __shfl_sync(0xffffffffu, f, i);
                     const float *src =
-                        a.part + ((int64_t)(2 * (k0 + i) + (k0 + i == c0 ? 1 : 0)) * rows + r) * D + lane * (D / 32);
+                        a.part + ((int64_t)(2 * (k0 + i) + (k0 + i == c0 ? 1 : 0)) * rows + r % rows) * D + lane * (D / 32);
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) acc[e] += src[e] * fi;
                 }

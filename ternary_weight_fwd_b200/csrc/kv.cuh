@@ -81,14 +81,14 @@ cudaError_t launch_append(const AppendArgs &a, int page_shift, dim3 grid, cudaSt
     }
 }
 
-// 3-D map of the codes: [page][kv head * token][D], boxes of 16 tokens of one head.
+// 3-D map of the codes: [page][kv head * token][D], boxes of one page's tokens of one head.
 bool encode_codes(CUtensorMap *map, const int8_t *codes, int64_t num_pages, int hk, int page_size, int d)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hk * page_size, (cuuint64_t)num_pages};
     cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)hk * page_size * d};
-    cuuint32_t box[3] = {(cuuint32_t)d, AT_GROUP, 1};
+    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)page_size, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(codes), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -113,7 +113,7 @@ bool encode_queries(CUtensorMap *map, const void *q, int64_t T, int64_t stride, 
 // ---- attention: choice of kernel and workspace ----------------------------------
 struct AttnPlan {
     bool ok;
-    int mt; // row tiles of 16 of the kernel for few tokens; 0: the kernel for prompts
+    int nq; // tiles of 8 rows of the kernel for few tokens (1 or 2); 0: the kernel for prompts
     size_t base_bytes, ml_bytes, part_bytes;
     size_t total() const { return base_bytes + ml_bytes + part_bytes; }
 };
@@ -125,8 +125,8 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d
         n_heads % hk != 0 || n_heads / hk > kMaxGroup || (d != 64 && d != 128) || max_new < 1 || max_new > T)
         return p;
     const int64_t rows = n_heads / hk * max_new;
-    p.mt = rows <= 16 ? 1 : rows <= AT_MAX_ROWS ? 2 : 0;
-    const size_t part_rows = (size_t)2 * AT_MAX_CTAS * (p.mt ? 16 * p.mt : AP_ROWS);
+    p.nq = rows <= 8 ? 1 : rows <= AT_MAX_ROWS ? 2 : 0;
+    const size_t part_rows = (size_t)2 * AT_MAX_CTAS * (p.nq ? 8 * p.nq : AP_ROWS);
     p.base_bytes = align_up((size_t)(n_seqs + 1) * 8, 256);
     p.ml_bytes = align_up(part_rows * sizeof(float2), 256);
     p.part_bytes = part_rows * d * sizeof(float);
@@ -134,18 +134,18 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d
     return p;
 }
 
-template <int D, int MT>
+template <int D, int NQ>
 cudaError_t launch_tokens(const CUtensorMap &tk, const CUtensorMap &tv, const AttnArgs &a, int ctas, int rows,
                           cudaStream_t stream, int dev)
 {
     static std::atomic<int> done[kMaxDevices];
-    constexpr int smem = at_smem(D, MT);
-    cudaError_t e = ensure_smem(k_attention_tokens<D, MT>, smem, done, dev);
+    constexpr int smem = at_smem(D, NQ);
+    cudaError_t e = ensure_smem(k_attention_tokens<D, NQ>, smem, done, dev);
     if (e == cudaSuccess)
-        e = launch_pdl(k_attention_tokens<D, MT>, dim3(ctas), dim3(AT_THREADS), smem, stream, tk, tv, a);
+        e = launch_pdl(k_attention_tokens<D, NQ>, dim3(ctas), dim3((at_warps(NQ) + 1) * 32), smem, stream, tk, tv, a);
     if (e == cudaSuccess)
         e = launch_pdl(k_attention_join<D>, dim3((unsigned)(a.bt.n_seqs * a.kv.hk), (unsigned)cdiv(rows, 4)),
-                       dim3(128), 0, stream, a, 16 * MT, ctas);
+                       dim3(128), 0, stream, a, 8 * NQ, ctas);
     return e;
 }
 
@@ -285,13 +285,13 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
     const int ctas = std::min(sms, AT_MAX_CTAS);
     const int rows = a.group * max_new;
     cudaError_t e;
-    if (p.mt == 0)
+    if (p.nq == 0)
         e = d == 128 ? launch_prompt<128>(tk, tv, a, ctas, stream, dev) : launch_prompt<64>(tk, tv, a, ctas, stream, dev);
     else if (d == 128)
-        e = p.mt == 1 ? launch_tokens<128, 1>(tk, tv, a, ctas, rows, stream, dev)
+        e = p.nq == 1 ? launch_tokens<128, 1>(tk, tv, a, ctas, rows, stream, dev)
                       : launch_tokens<128, 2>(tk, tv, a, ctas, rows, stream, dev);
     else
-        e = p.mt == 1 ? launch_tokens<64, 1>(tk, tv, a, ctas, rows, stream, dev)
+        e = p.nq == 1 ? launch_tokens<64, 1>(tk, tv, a, ctas, rows, stream, dev)
                       : launch_tokens<64, 2>(tk, tv, a, ctas, rows, stream, dev);
     return cuda_status(e);
 }
