@@ -258,7 +258,7 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
     if (tid == 0) {
         for (int s = 0; s < AT_STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], AT_GROUPS); // one arrival per group, by the warp that took it
+            mbar_init(&empty[s], WARPS);
         }
         fence_mbarrier_init();
     }
@@ -408,7 +408,12 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
     const int key_g = (g & 1) ? ((g + 4) & 7) : g;      // token of score row g (g + 8: + 8): 0 5 2 7 4 1 6 3, see below
     const int key_e = 2 * c, key_o = (2 * c + 5) & 7;   // tokens of contraction indices 2c, 2c + 1 of the second product
     const uint32_t q_base = smem_u32(s_q), ring_base = smem_u32(ring);
-    int n = warp; // this warp's next group, counted from the CTA's first chunk
+    // Every warp waits for and releases every chunk, with or without a group of its own in it:
+    // none is then ever a whole turn of the ring away from another, where a phase's parity
+    // would say the opposite.
+    int n = warp;  // this warp's next group, counted from the CTA's first chunk
+    int stage = 0;
+    uint32_t phase = 0;
     bool ok = true;
     auto sync_consumers = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
 
@@ -485,15 +490,14 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
         }
         float unit = 0.0f, inv_unit = 0.0f; // o is in units of this power of two; 0: not chosen yet
 
-        const int n_end = (int)(u - u0 + cnt) * AT_GROUPS;
-        for (; n < n_end; n += WARPS) {
-            const int chunk = n / AT_GROUPS;
-            const int member = (int)(n % AT_GROUPS), st = (int)(chunk % AT_STAGES);
-            ok = __all_sync(0xffffffffu, ok && kv_wait(&full[st], (uint32_t)(chunk / AT_STAGES) & 1u));
-            const int key0 = (t0 + chunk - (int)(u - u0)) * AT_CHUNK + member * AT_GROUP;
-            if (ok && key0 < len) {
-                const float ks = s_step[st * 16 + member], vs = s_step[st * 16 + 8 + member];
-                const uint32_t kb = ring_base + st * 2 * TILE + member * AT_GROUP * D, vb = kb + TILE;
+        for (int i = 0; i < cnt; ++i) {
+            ok = __all_sync(0xffffffffu, ok && kv_wait(&full[stage], phase));
+            const int member = n - ((int)(u - u0) + i) * AT_GROUPS; // this warp's group of the chunk, if below 8
+            const int key0 = (t0 + i) * AT_CHUNK + member * AT_GROUP;
+            if (member < AT_GROUPS) n += WARPS;
+            if (ok && member < AT_GROUPS && key0 < len) {
+                const float ks = s_step[stage * 16 + member], vs = s_step[stage * 16 + 8 + member];
+                const uint32_t kb = ring_base + stage * 2 * TILE + member * AT_GROUP * D, vb = kb + TILE;
                 float s[NQ][4];
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
@@ -623,7 +627,11 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[st]);
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == AT_STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
 
         // ---- join the warps ----
