@@ -7,30 +7,31 @@
 //
 // Bound by HBM: the codes of K and V are read once (2 D bytes per cached token
 // and kv head; everything else is small).  The work is the list of all
-// (sequence, kv head, tile of 8 or 16 rows, chunk of 128 tokens) in that order,
-// cut into equal contiguous shares, one per CTA (one CTA per SM), so ragged
-// batches and single long sequences load every SM alike.  A share's partial
-// softmax of a row tile that it does not hold whole goes to the workspace (at
-// most two per CTA) and k_attention_join adds them up in the order of the CTAs:
-// no atomics, the result does not depend on timing.
+// (sequence, kv head, tile of 8 or 16 rows, group of 16 tokens) in that order,
+// cut into equal contiguous shares, one per CTA (one CTA per SM), and those into
+// equal shares per warp, so ragged batches and single long sequences load every
+// SM alike.  A warp works alone: it copies its groups' codes into its own two
+// buffers in shared memory, the next while it computes on one, keeps its own
+// running maxima and sums, and waits for no other warp before the end.  Then the
+// CTA adds up the pieces of (sequence, kv head, row tile) that its warps share, in
+// the order of the warps; what it shares with other CTAs (at most two) goes to the
+// workspace, and k_attention_join adds that up in the order of the CTAs: no
+// atomics, the result does not depend on timing.
+// (Before, a producer warp fed all warps through one ring by TMA, and the warps
+// joined at the end of every row tile: 70 us for 64 sequences of up to 4096 tokens,
+// 51 us of them without any computation; 16-token pages, a TMA each, took longer
+// still.)
 //
-// Within a CTA a producer warp streams chunks through a ring in shared memory by
-// TMA, a box per page.  The other warps
-// take the groups of 16 tokens in turn, each with running maxima and sums of its
-// own, joined once per row tile: as many warps as their registers allow (15 for
-// tiles of 8 rows, 11 for 16), since one warp's chain of loads, products and
-// exponentials leaves most of its time unused.
 // The products run on mma.sync m16n8k16 in fp16 with fp32 sums and the tokens
 // (K) and the head dimension (V transposed) on the side of 16, the rows on the
 // side of 8: a row tile needs half the instructions and registers that it would
-// with its rows on the side of 16, and what costs here is instructions per byte
-// of codes (rows on 16 with eight warps: 51 us for one sequence of 131071 tokens,
-// 3.3 TB/s).  Codes are exact in fp16 (the byte goes under the exponent of 1024
-// and 1152 is subtracted), queries are brought into fp16's range by a power of two
-// per row.  K and V fragments are read from the ring in the layout that the bytes
-// already have: an order of the contraction index and of the output rows can be
-// chosen freely, so a lane takes 16 consecutive bytes of a key (K) or of a value
-// (V).
+// with its rows on the side of 16, and instructions per byte of codes are what
+// costs besides HBM.  Codes are exact in fp16 (the byte goes under the exponent of
+// 1024 and 1152 is subtracted), queries are brought into fp16's range by a power of
+// two per row.  K and V fragments are read from shared memory in the layout that
+// the bytes already have: an order of the contraction index and of the output rows
+// can be chosen freely, so a lane takes 16 consecutive bytes of a key (K) or of a
+// value (V).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -39,14 +40,11 @@
 
 namespace bitnet {
 
-constexpr int AT_CHUNK = 128;   // tokens per ring stage
-constexpr int AT_GROUP = 16;    // tokens a warp takes at a time (a page holds at least as many)
-constexpr int AT_GROUPS = AT_CHUNK / AT_GROUP;
-constexpr int AT_STAGES = 5;
+constexpr int AT_GROUP = 16;    // tokens a warp takes at a time (a page holds at least as many): a unit
 constexpr int AT_MAX_ROWS = 32; // query rows per (sequence, kv head)
 constexpr int AT_MAX_CTAS = 160;
-constexpr int AT_MIN_UNITS = 2; // chunks worth a CTA of their own
-constexpr float AT_LAZY = 8.0f; // a row's exponents refer to a maximum up to 2^8 behind
+constexpr int AT_MIN_UNITS = 16; // groups worth a CTA of their own
+constexpr float AT_LAZY = 8.0f;  // a row's exponents refer to a maximum up to 2^8 behind
 
 struct AttnArgs {
     KvView kv;
@@ -63,13 +61,12 @@ struct AttnArgs {
     int64_t *base;     // [n_seqs + 1] first unit of each sequence
 };
 
-// Consumer warps for nq tiles of 8 rows; with the producer they fill 16 (12) warps of 128 (168) registers.
-constexpr __host__ __device__ int at_warps(int nq) { return nq == 1 ? 15 : 11; }
+// Warps for nq tiles of 8 rows: as many as their registers allow (128, 168).
+constexpr __host__ __device__ int at_warps(int nq) { return nq == 1 ? 16 : 12; }
 
 constexpr __host__ __device__ int at_smem(int d, int nq)
 {
-    return 1024 + AT_STAGES * 2 * AT_CHUNK * d + 8 * nq * (2 * d + 16) + at_warps(nq) * 8 * nq * (36 * 4 + 8) +
-           8 * nq * 8 + 1024;
+    return 4096 + at_warps(nq) * (2 * 2 * AT_GROUP * d + 8 * nq * (d + 4) * 4 + 2 * 8 * nq * 8) + 1024;
 }
 
 // 3-D tiled tensor copy global -> shared (no multicast); c0 is 0 here.
@@ -81,6 +78,11 @@ BITNET_DEVINL void tma_load_3d(uint32_t dst_smem, const CUtensorMap *map, int32_
         "[%5];" ::"r"(dst_smem),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
+}
+
+BITNET_DEVINL void cp_async16_u32(uint32_t dst_smem, const void *src_gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src_gmem) : "memory");
 }
 
 BITNET_DEVINL uint4 lds128(uint32_t addr)
@@ -176,9 +178,9 @@ BITNET_DEVINL AttnSeq attn_seq(const AttnArgs &a, int b)
     return s;
 }
 
-BITNET_DEVINL int attn_chunks(const AttnSeq &s) { return s.n > 0 ? (s.len + AT_CHUNK - 1) / AT_CHUNK : 0; }
+BITNET_DEVINL int attn_groups(const AttnSeq &s) { return s.n > 0 ? (s.len + AT_GROUP - 1) / AT_GROUP : 0; }
 
-// CTAs that share `units` chunks.
+// CTAs that share `units` groups.
 BITNET_DEVINL int64_t attn_active(int64_t units, int ctas)
 {
     const int64_t want = (units + AT_MIN_UNITS - 1) / AT_MIN_UNITS;
@@ -189,7 +191,7 @@ BITNET_DEVINL int64_t attn_active(int64_t units, int ctas)
 BITNET_DEVINL int attn_row_tiles(const AttnArgs &a, const AttnSeq &s, int rows) { return (s.n * a.group + rows - 1) / rows; }
 BITNET_DEVINL int64_t attn_units(const AttnArgs &a, const AttnSeq &s, int rows)
 {
-    return (int64_t)a.kv.hk * attn_row_tiles(a, s, rows) * attn_chunks(s);
+    return (int64_t)a.kv.hk * attn_row_tiles(a, s, rows) * attn_groups(s);
 }
 
 // Walks the unit list: sequence of unit u, given a sequence at or before it.
@@ -197,12 +199,12 @@ struct UnitIter {
     int b;
     int64_t base; // first unit of sequence b
     AttnSeq s;
-    int nc, nt;   // chunks, row tiles per kv head
+    int nc, nt;   // groups, row tiles per kv head
 
     BITNET_DEVINL void load(const AttnArgs &a, int rows)
     {
         s = attn_seq(a, b);
-        nc = attn_chunks(s);
+        nc = attn_groups(s);
         nt = attn_row_tiles(a, s, rows);
     }
     BITNET_DEVINL void seek(const AttnArgs &a, int64_t u, int rows)
@@ -217,59 +219,48 @@ struct UnitIter {
     }
 };
 
-// Byte offset of 16-byte chunk c of row r in a tile of D-byte rows as the TMA's
-// swizzle leaves it (128-byte swizzle for D = 128, 64-byte for D = 64).
+// Byte offset of 16-byte chunk c of row r in a tile of D-byte rows, as TMA's
+// 128-byte (D = 128) and 64-byte (D = 64) swizzles place it.
 template <int D>
 BITNET_DEVINL uint32_t kv_swz(int r, int c)
 {
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// A warp's share of a row tile that it does not hold whole.
+struct AtPiece {
+    int64_t first, end; // units of the row tile; first = -1: no piece
+    int q0, h, r0, nrow;
+};
+
 // NQ: tiles of 8 query rows.
 template <int D, int NQ>
-__global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
-    k_attention_tokens(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const AttnArgs a)
+__global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const AttnArgs a)
 {
-    constexpr int WARPS = at_warps(NQ), THREADS = (WARPS + 1) * 32;
+    constexpr int WARPS = at_warps(NQ), THREADS = WARPS * 32;
     constexpr int DT = D / 16;              // output tiles of 16 elements
     constexpr int ROWS = 8 * NQ;
-    constexpr uint32_t TILE = AT_CHUNK * D; // bytes of K (or V) per stage
-    constexpr int QROW = 2 * D + 16;        // bytes of a query row in shared memory
-    constexpr int MROW = 36;                // floats of a row of the join buffer
+    constexpr uint32_t TILE = AT_GROUP * D; // bytes of K (or V) of a group
+    constexpr int PROW = D + 4;             // floats of a row of a piece
+    constexpr int CPR = D / 16;             // 16-byte chunks of a token
+    constexpr int COPIES = AT_GROUP * CPR / 32;
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem);
-    uint64_t *empty = full + AT_STAGES;
-    int64_t *s_u = reinterpret_cast<int64_t *>(empty + AT_STAGES); // first sequence's base
-    int *s_b = reinterpret_cast<int *>(s_u + 1);
-    float *s_step = reinterpret_cast<float *>(smem + 128);        // [stages][2][8]
-    int64_t *s_scan = reinterpret_cast<int64_t *>(smem + 640);    // [WARPS + 1] warp sums
-    unsigned char *ring = smem + 1024;
-    unsigned char *s_q = ring + AT_STAGES * 2 * TILE;
-    float *s_join = reinterpret_cast<float *>(s_q + ROWS * QROW);               // [WARPS][ROWS][36]
-    float2 *s_ml = reinterpret_cast<float2 *>(s_join + WARPS * ROWS * MROW);    // [WARPS][ROWS]
-    float *s_fac = reinterpret_cast<float *>(s_ml + WARPS * ROWS);              // [ROWS] score factor
-    int *s_lim = reinterpret_cast<int *>(s_fac + ROWS);                         // [ROWS] last visible position
+    int64_t *s_scan = reinterpret_cast<int64_t *>(smem);            // [WARPS] sums
+    AtPiece *s_piece = reinterpret_cast<AtPiece *>(smem + 256);     // [WARPS][2]
+    float2 *s_step = reinterpret_cast<float2 *>(smem + 256 + 32 * 32 + 256); // [WARPS][2 buffers] k_step, v_step
+    unsigned char *ring = smem + 4096;                              // [WARPS][2 buffers][K, V]
+    float *s_first = reinterpret_cast<float *>(ring + WARPS * 4 * TILE); // [WARPS][ROWS][PROW]: first pieces
+    float2 *s_ml = reinterpret_cast<float2 *>(s_first + WARPS * ROWS * PROW); // [WARPS][2][ROWS]
+    static_assert(WARPS <= 16 && sizeof(AtPiece) == 32 && 256 + 1024 + 256 + 16 * 2 * 8 <= 4096, "layout");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int s = 0; s < AT_STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], WARPS);
-        }
-        fence_mbarrier_init();
-    }
-    if (tid == WARPS * 32) {
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
-    }
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- total units, this CTA's share and the sequence it starts in ----
+    // ---- total units, this CTA's and this warp's share and the sequence that it starts in ----
     const int per = (a.bt.n_seqs + THREADS - 1) / THREADS;
     const int b_lo = min(a.bt.n_seqs, tid * per), b_hi = min(a.bt.n_seqs, b_lo + per);
     int64_t mine = 0;
@@ -281,16 +272,17 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
         if (lane >= o) incl += up;
     }
     if (lane == 31) s_scan[warp] = incl;
+    if (tid < WARPS * 2) s_piece[tid].first = -1;
     __syncthreads();
     int64_t before = incl - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w <= WARPS; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
     const int64_t active = attn_active(total, gridDim.x);
     const bool idle = blockIdx.x >= active;
-    const int64_t u0 = idle ? 0 : total * blockIdx.x / active, u1 = idle ? 0 : total * (blockIdx.x + 1) / active;
+    const int64_t c0 = idle ? 0 : total * blockIdx.x / active, c1 = idle ? 0 : total * (blockIdx.x + 1) / active;
     if (blockIdx.x == 0) { // the join kernel reads the units' bases
         int64_t at = before;
         for (int b = b_lo; b < b_hi; ++b) {
@@ -300,11 +292,14 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
         if (tid == 0) a.base[a.bt.n_seqs] = total;
     }
     if (idle) return;
-    if (u0 >= before && u0 < before + mine) {
+    // where the CTA starts; its warps walk on from there
+    int *s_b = reinterpret_cast<int *>(s_step);
+    int64_t *s_u = reinterpret_cast<int64_t *>(s_step) + 1;
+    if (c0 >= before && c0 < before + mine) {
         int64_t at = before;
         for (int b = b_lo; b < b_hi; ++b) {
             const int64_t un = attn_units(a, attn_seq(a, b), ROWS);
-            if (u0 < at + un) {
+            if (c0 < at + un) {
                 s_b[0] = b;
                 s_u[0] = at;
                 break;
@@ -317,187 +312,133 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
     it.b = s_b[0];
     it.base = s_u[0];
     it.load(a, ROWS);
+    __syncthreads(); // s_step is the warps' own from here on
 
-    if (warp == WARPS) {
-        // ---------------- producer ----------------
-        // A batch of four chunks: lane = chunk * 8 + 16-token group.  Page ids are
-        // fetched two batches ahead and steps one batch ahead of their copies.
-        const int sub = lane >> 3, grp = lane & 7, page_size = 1 << a.kv.page_shift;
-        int page1 = -1, row1 = 0; // next batch
-        bool valid1 = false;
-        auto fetch = [&](int64_t u, int &page, int &row, bool &valid) {
-            valid = false;
-            page = -1;
-            row = 0;
-            if (u < u1) {
-                it.seek(a, u, ROWS);
-                const int rel = (int)(u - it.base);
-                const int ht = rel / it.nc, key0 = (rel - ht * it.nc) * AT_CHUNK + grp * AT_GROUP;
-                if (key0 < it.s.len) {
-                    valid = true;
-                    page = page_of(a.kv, a.bt, it.b, key0 >> a.kv.page_shift);
-                    row = ((ht / it.nt) << a.kv.page_shift) + (key0 & ((1 << a.kv.page_shift) - 1));
-                }
+    const int64_t u0 = c0 + (c1 - c0) * warp / WARPS, u1 = c0 + (c1 - c0) * (warp + 1) / WARPS;
+    const uint32_t ring_base = smem_u32(ring) + warp * 4 * TILE;
+    float2 *steps = s_step + warp * 2;
+
+    // ---- copies ----
+    // 32 groups at a time, a lane looks up a group's page and steps, one such batch ahead.
+    UnitIter ahead = it;
+    auto look_up = [&](int64_t u, int64_t &row, float &ks, float &vs) { // row of the codes' [page][head][slot], or -1
+        row = -1;
+        ks = vs = 0.0f;
+        if (u >= u1) return;
+        ahead.seek(a, u, ROWS);
+        const int64_t rel = u - ahead.base;
+        const int ht = (int)(rel / ahead.nc), key0 = (int)(rel - (int64_t)ht * ahead.nc) * AT_GROUP;
+        const int page = page_of(a.kv, a.bt, ahead.b, key0 >> a.kv.page_shift);
+        if (page < 0) return;
+        const int64_t at = (int64_t)page * a.kv.hk + ht / ahead.nt;
+        row = (at << a.kv.page_shift) + (key0 & ((1 << a.kv.page_shift) - 1));
+        ks = a.kv.k_step[at];
+        vs = a.kv.v_step[at];
+    };
+    int64_t row_a, row_b;
+    float ks_a, vs_a, ks_b, vs_b;
+    look_up(u0 + lane, row_a, ks_a, vs_a);
+    look_up(u0 + 32 + lane, row_b, ks_b, vs_b);
+    int issued = 0; // groups whose copies are under way or done
+    auto copy = [&]() {
+        const int from = issued & 31, buf = issued & 1;
+        const int64_t row = __shfl_sync(0xffffffffu, row_a, from);
+        const float ks = __shfl_sync(0xffffffffu, ks_a, from), vs = __shfl_sync(0xffffffffu, vs_a, from);
+        if (row >= 0) {
+            const int8_t *k = a.kv.k + row * D + lane * 16, *v = a.kv.v + row * D + lane * 16;
+            const uint32_t dst = ring_base + buf * 2 * TILE;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+                const int x = lane + 32 * i;
+                const uint32_t at = dst + kv_swz<D>(x / CPR, x % CPR);
+                cp_async16_u32(at, k + i * 512);
+                cp_async16_u32(at + TILE, v + i * 512);
             }
-        };
-        int page = -1, row = 0;
-        bool valid = false;
-        fetch(u0 + sub, page, row, valid);
-        float ks = 0.0f, vs = 0.0f, ks1 = 0.0f, vs1 = 0.0f;
-        auto steps = [&](int pg, int rw, float &k, float &v) {
-            k = v = 0.0f;
-            if (pg >= 0) {
-                const int64_t at = (int64_t)pg * a.kv.hk + (rw >> a.kv.page_shift);
-                k = a.kv.k_step[at];
-                v = a.kv.v_step[at];
-            }
-        };
-        steps(page, row, ks, vs);
-        fetch(u0 + 4 + sub, page1, row1, valid1);
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, last_par = 0;
-        bool ok = true;
-        for (int64_t u = u0; u < u1 && ok; u += 4) {
-            steps(page1, row1, ks1, vs1);
-            int page2, row2;
-            bool valid2;
-            fetch(u + 8 + sub, page2, row2, valid2);
-#pragma unroll 1
-            for (int s = 0; s < 4 && u + s < u1; ++s) {
-                ok = __all_sync(0xffffffffu, kv_wait(&empty[stage], phase ^ 1));
-                if (!ok) break;
-                const bool here = sub == s && valid;
-                if (here) {
-                    s_step[stage * 16 + grp] = ks;
-                    s_step[stage * 16 + 8 + grp] = vs;
-                }
-                const bool copy = here && page >= 0 && (grp * AT_GROUP & (page_size - 1)) == 0; // a page's first group
-                const int copies = __popc(__ballot_sync(0xffffffffu, copy));
-                __syncwarp(); // the steps are written before the arrival that shows them
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], copies * 2 * page_size * D);
-                __syncwarp();
-                if (copy) {
-                    const uint32_t dst = smem_u32(ring) + stage * 2 * TILE + grp * AT_GROUP * D;
-                    tma_load_3d(dst, &tm_k, 0, row, page, &full[stage]);
-                    tma_load_3d(dst + TILE, &tm_v, 0, row, page, &full[stage]);
-                }
-                issued |= 1u << stage;
-                last_par = (last_par & ~(1u << stage)) | (phase << stage);
-                if (++stage == AT_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-            page = page1;
-            row = row1;
-            valid = valid1;
-            ks = ks1;
-            vs = vs1;
-            page1 = page2;
-            row1 = row2;
-            valid1 = valid2;
         }
-        // let every copy this CTA issued land before the CTA can exit
-        for (int s = 0; s < AT_STAGES; ++s)
-            if (issued & (1u << s)) mbar_wait_drain(&full[s], (last_par >> s) & 1);
-        return;
-    }
+        if (lane == 0) steps[buf] = make_float2(ks, vs);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++issued;
+        if ((issued & 31) == 0) {
+            row_a = row_b;
+            ks_a = ks_b;
+            vs_a = vs_b;
+            look_up(u0 + issued + 32 + lane, row_b, ks_b, vs_b);
+        }
+    };
+    copy();
+    copy();
 
-    // ---------------- consumers ----------------
     const int g = lane >> 2, c = lane & 3;
     const int key_g = (g & 1) ? ((g + 4) & 7) : g;      // token of score row g (g + 8: + 8): 0 5 2 7 4 1 6 3, see below
     const int key_e = 2 * c, key_o = (2 * c + 5) & 7;   // tokens of contraction indices 2c, 2c + 1 of the second product
-    const uint32_t q_base = smem_u32(s_q), ring_base = smem_u32(ring);
-    // Every warp waits for and releases every chunk, with or without a group of its own in it:
-    // none is then ever a whole turn of the ring away from another, where a phase's parity
-    // would say the opposite.
-    int n = warp;  // this warp's next group, counted from the CTA's first chunk
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    auto sync_consumers = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
+    int done = 0; // groups consumed
 
     for (int64_t u = u0; u < u1;) {
         it.seek(a, u, ROWS);
-        const int rel = (int)(u - it.base);
-        const int ht = rel / it.nc, t0 = rel - ht * it.nc;
+        const int64_t rel = u - it.base;
+        const int ht = (int)(rel / it.nc), t0 = (int)(rel - (int64_t)ht * it.nc);
         const int h = ht / it.nt, r0 = (ht - h * it.nt) * ROWS; // kv head, first row of the tile
         const int cnt = (int)min((int64_t)(it.nc - t0), u1 - u);
         const int nrow = min(ROWS, it.s.n * a.group - r0);
         const int len = it.s.len, first = len - it.s.n;
 
-        // queries of this row tile, scaled into fp16's range row by row
-        for (int r = warp; r < ROWS; r += WARPS) {
-            float x[D / 32];
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) x[e] = 0.0f;
-            const int tok = (r0 + r) / a.group;
-            if (r < nrow) {
-                const uint16_t *p = a.q + (int64_t)(it.s.q0 + tok) * a.q_stride +
-                                    ((int64_t)h * a.group + (r0 + r - tok * a.group)) * D + lane * (D / 32);
-                if constexpr (D == 128) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-                    x[0] = bf16_bits_lo(w.x);
-                    x[1] = bf16_bits_hi(w.x);
-                    x[2] = bf16_bits_lo(w.y);
-                    x[3] = bf16_bits_hi(w.y);
-                } else {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-                    x[0] = bf16_bits_lo(w);
-                    x[1] = bf16_bits_hi(w);
-                }
-            }
-            float mx = 0.0f;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) mx = fmaxf(mx, fabsf(x[e]));
-            mx = warp_max(mx);
-            const float f = half_range_factor(mx);
-            uint32_t *dst = reinterpret_cast<uint32_t *>(s_q + r * QROW + lane * (D / 16));
-#pragma unroll
-            for (int e = 0; e < D / 64; ++e) dst[e] = pack_half2(x[2 * e] * f, x[2 * e + 1] * f);
-            if (lane == 0) {
-                s_fac[r] = a.scale_log2 / f;
-                s_lim[r] = r < nrow ? first + tok : -1;
-            }
-        }
-        sync_consumers();
-
-        // rows of this lane: 8 t + 2 c and + 1 (scores and weights), 8 t + g (queries)
+        // queries of this row tile, scaled into fp16's range row by row.  Rows of this lane: 8 t + g
+        // (queries), 8 t + 2 c and + 1 (scores and weights).
         uint32_t qb[NQ][D / 64][8]; // contraction step 4 hh + w: qb[t][hh][2 w], [2 w + 1]
         float o[NQ][DT][4], m[NQ][2], l[NQ][2], fac[NQ][2];
         int lim[NQ][2];
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
+            const int r = 8 * t + g, tok = (r0 + r) / a.group;
+            const bool live = r < nrow;
+            const uint16_t *p = a.q + (int64_t)(it.s.q0 + (live ? tok : 0)) * a.q_stride +
+                                ((int64_t)h * a.group + (live ? r0 + r - tok * a.group : 0)) * D + c * 16;
+            uint4 w[D / 64][2];
+            float mx = 0.0f;
 #pragma unroll
             for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint4 w = lds128(q_base + (8 * t + g) * QROW + (c + 4 * hh) * 32 + 16 * e);
-                    qb[t][hh][4 * e] = w.x;
-                    qb[t][hh][4 * e + 1] = w.y;
-                    qb[t][hh][4 * e + 2] = w.z;
-                    qb[t][hh][4 * e + 3] = w.w;
-                }
+                    w[hh][e] = live ? *reinterpret_cast<const uint4 *>(p + 64 * hh + 8 * e) : make_uint4(0, 0, 0, 0);
+                    const uint32_t v[4] = {w[hh][e].x, w[hh][e].y, w[hh][e].z, w[hh][e].w};
 #pragma unroll
-            for (int n = 0; n < DT; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
+                    for (int i = 0; i < 4; ++i)
+                        mx = fmaxf(mx, fmaxf(fabsf(bf16_bits_lo(v[i])), fabsf(bf16_bits_hi(v[i]))));
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float f = half_range_factor(mx);
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t v[4] = {w[hh][e].x, w[hh][e].y, w[hh][e].z, w[hh][e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        qb[t][hh][4 * e + i] = pack_half2(bf16_bits_lo(v[i]) * f, bf16_bits_hi(v[i]) * f);
+                }
+            const float fr = a.scale_log2 / f;
+            const int lr = live ? first + tok : -1; // last visible position
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                fac[t][e] = __shfl_sync(0xffffffffu, fr, 4 * (2 * c + e));
+                lim[t][e] = __shfl_sync(0xffffffffu, lr, 4 * (2 * c + e));
                 m[t][e] = -INFINITY;
                 l[t][e] = 0.0f;
-                fac[t][e] = s_fac[8 * t + 2 * c + e];
-                lim[t][e] = s_lim[8 * t + 2 * c + e];
             }
+#pragma unroll
+            for (int n = 0; n < DT; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
         }
         float unit = 0.0f, inv_unit = 0.0f; // o is in units of this power of two; 0: not chosen yet
 
         for (int i = 0; i < cnt; ++i) {
-            ok = __all_sync(0xffffffffu, ok && kv_wait(&full[stage], phase));
-            const int member = n - ((int)(u - u0) + i) * AT_GROUPS; // this warp's group of the chunk, if below 8
-            const int key0 = (t0 + i) * AT_CHUNK + member * AT_GROUP;
-            if (member < AT_GROUPS) n += WARPS;
-            if (ok && member < AT_GROUPS && key0 < len) {
-                const float ks = s_step[stage * 16 + member], vs = s_step[stage * 16 + 8 + member];
-                const uint32_t kb = ring_base + stage * 2 * TILE + member * AT_GROUP * D, vb = kb + TILE;
+            asm volatile("cp.async.wait_group 1;" ::: "memory"); // all but the newest copies
+            __syncwarp();
+            const int key0 = (t0 + i) * AT_GROUP;
+            {
+                const float2 step = steps[done & 1];
+                const float ks = step.x, vs = step.y;
+                const uint32_t kb = ring_base + (done & 1) * 2 * TILE, vb = kb + TILE;
                 float s[NQ][4];
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
@@ -626,86 +567,117 @@ __global__ void __launch_bounds__((at_warps(NQ) + 1) * 32, 1)
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (++stage == AT_STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
+            __syncwarp(); // the buffer has been read
+            copy();
+            ++done;
         }
 
-        // ---- join the warps ----
+        // ---- sums of the lanes; the piece or the result ----
 #pragma unroll
         for (int t = 0; t < NQ; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], x);
-                if (g == 0) s_ml[warp * ROWS + 8 * t + 2 * c + e] = make_float2(m[t][e], l[t][e]);
-            }
-        sync_consumers();
-        float wf[NQ][2]; // this warp's weight of its rows
-#pragma unroll
-        for (int t = 0; t < NQ; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mm = -INFINITY;
-                for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, s_ml[w * ROWS + 8 * t + 2 * c + e].x);
-                wf[t][e] = m[t][e] == -INFINITY ? 0.0f : fast_exp2(m[t][e] - mm) * unit;
-            }
-        const bool whole = cnt == it.nc;
-        const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-        // thread -> (row, eighth of the head dimension) of the result
-        const int jr = tid >> 3, jn = tid & 7;
-        float jm = -INFINITY, jl = 0.0f;
-        if (jr < nrow) {
-            for (int w = 0; w < WARPS; ++w) jm = fmaxf(jm, s_ml[w * ROWS + jr].x);
-            if (jm != -INFINITY)
-                for (int w = 0; w < WARPS; ++w) {
-                    const float2 x = s_ml[w * ROWS + jr];
-                    jl += x.y * fast_exp2(x.x - jm);
-                }
-            if (!whole && jn == 0) a.part_ml[(int64_t)slot * ROWS + jr] = make_float2(jm, jl);
-        }
-        const float inv = jl > 0.0f ? 1.0f / jl : 0.0f;
-        const int jtok = (r0 + jr) / a.group;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            if (w) sync_consumers();
+        if (cnt == it.nc) {
 #pragma unroll
             for (int t = 0; t < NQ; ++t)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (8 * t + 2 * c + e < nrow)
-                        *reinterpret_cast<float4 *>(s_join + (warp * ROWS + 8 * t + 2 * c + e) * MROW + g * 4) =
-                            make_float4(o[t][2 * w][e] * wf[t][e], o[t][2 * w][2 + e] * wf[t][e],
-                                        o[t][2 * w + 1][e] * wf[t][e], o[t][2 * w + 1][2 + e] * wf[t][e]);
-            sync_consumers();
-            if (jr < nrow) {
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * t + 2 * c + e;
+                    if (r >= nrow) continue;
+                    const float inv = m[t][e] > -INFINITY ? unit / l[t][e] : 0.0f;
+                    const int tok = (r0 + r) / a.group;
+                    uint16_t *p = a.out + (int64_t)(it.s.q0 + tok) * a.out_stride +
+                                  ((int64_t)h * a.group + (r0 + r - tok * a.group)) * D + (D / 8) * g;
+                    uint32_t w[DT];
 #pragma unroll
-                for (int k = 0; k < WARPS; ++k) {
-                    const float4 y = *reinterpret_cast<const float4 *>(s_join + (k * ROWS + jr) * MROW + jn * 4);
-                    x.x += y.x;
-                    x.y += y.y;
-                    x.z += y.z;
-                    x.w += y.w;
+                    for (int n = 0; n < DT; ++n)
+                        w[n] = bf16_rn_bits(o[t][n][e] * inv) | (bf16_rn_bits(o[t][n][2 + e] * inv) << 16);
+#pragma unroll
+                    for (int n = 0; n < DT; n += 4)
+                        *reinterpret_cast<uint4 *>(p + 2 * n) = make_uint4(w[n], w[n + 1], w[n + 2], w[n + 3]);
                 }
-                const int d = (D / 8) * jn + 4 * w;
-                if (whole) {
-                    uint16_t *p = a.out + (int64_t)(it.s.q0 + jtok) * a.out_stride +
-                                  ((int64_t)h * a.group + (r0 + jr - jtok * a.group)) * D + d;
-                    *reinterpret_cast<uint2 *>(p) =
-                        make_uint2(bf16_rn_bits(x.x * inv) | (bf16_rn_bits(x.y * inv) << 16),
-                                   bf16_rn_bits(x.z * inv) | (bf16_rn_bits(x.w * inv) << 16));
-                } else {
-                    *reinterpret_cast<float4 *>(a.part + ((int64_t)slot * ROWS + jr) * D + d) = x;
+        } else {
+            // the first piece beside the buffers; a later one is the warp's last and takes their place
+            const int k = u == u0 ? 0 : 1;
+            if (k) asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            float *dst = k ? reinterpret_cast<float *>(ring + warp * 4 * TILE) : s_first + warp * ROWS * PROW;
+            const int prow = k ? D : PROW;
+#pragma unroll
+            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * t + 2 * c + e;
+#pragma unroll
+                    for (int n = 0; n < DT; n += 2)
+                        *reinterpret_cast<float4 *>(dst + r * prow + (D / 8) * g + 2 * n) =
+                            make_float4(o[t][n][e] * unit, o[t][n][2 + e] * unit, o[t][n + 1][e] * unit,
+                                        o[t][n + 1][2 + e] * unit);
+                    if (g == 0) s_ml[(warp * 2 + k) * ROWS + r] = make_float2(m[t][e], l[t][e]);
                 }
+            if (lane == 0) {
+                AtPiece &pc = s_piece[warp * 2 + k];
+                pc.first = it.base + (int64_t)ht * it.nc;
+                pc.end = pc.first + it.nc;
+                pc.q0 = it.s.q0;
+                pc.h = h;
+                pc.r0 = r0;
+                pc.nrow = nrow;
             }
         }
         u += cnt;
-        // the next pass writes s_q, s_fac, s_lim (not read any more) and only after its own
-        // barrier anything that this one still reads
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+
+    // ---- pieces of the same row tile, in the order of the warps; a warp per row ----
+    for (int p0 = 0; p0 < WARPS * 2;) {
+        const AtPiece pc = s_piece[p0];
+        if (pc.first < 0) {
+            ++p0;
+            continue;
+        }
+        int p1 = p0 + 1; // behind the last piece of this row tile (the next pieces that exist)
+        while (p1 < WARPS * 2 && (s_piece[p1].first < 0 || s_piece[p1].first == pc.first)) ++p1;
+        const bool whole = pc.first >= c0 && pc.end <= c1;
+        const int slot = 2 * blockIdx.x + (pc.first >= c0 ? 1 : 0);
+        for (int r = warp; r < pc.nrow; r += WARPS) {
+            float mm = -INFINITY;
+            for (int p = p0; p < p1; ++p)
+                if (s_piece[p].first >= 0) mm = fmaxf(mm, s_ml[p * ROWS + r].x);
+            float ll = 0.0f, acc[D / 32];
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+            if (mm > -INFINITY)
+                for (int p = p0; p < p1; ++p) {
+                    if (s_piece[p].first < 0) continue;
+                    const float2 ml = s_ml[p * ROWS + r];
+                    const float f = fast_exp2(ml.x - mm);
+                    const float *src = (p & 1) ? reinterpret_cast<const float *>(ring + (p >> 1) * 4 * TILE) + r * D
+                                               : s_first + (p >> 1) * ROWS * PROW + r * PROW;
+                    ll += ml.y * f;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) acc[e] += src[lane * (D / 32) + e] * f;
+                }
+            if (whole) {
+                const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+                const int tok = (pc.r0 + r) / a.group;
+                uint32_t *p = reinterpret_cast<uint32_t *>(a.out + (int64_t)(pc.q0 + tok) * a.out_stride +
+                                                           ((int64_t)pc.h * a.group + (pc.r0 + r - tok * a.group)) * D) +
+                              lane * (D / 64);
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e)
+                    p[e] = bf16_rn_bits(acc[2 * e] * inv) | (bf16_rn_bits(acc[2 * e + 1] * inv) << 16);
+            } else {
+                float *p = a.part + ((int64_t)slot * ROWS + r) * D + lane * (D / 32);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) p[e] = acc[e];
+                if (lane == 0) a.part_ml[(int64_t)slot * ROWS + r] = make_float2(mm, ll);
+            }
+        }
+        p0 = p1;
     }
 }
 
@@ -723,7 +695,7 @@ __global__ void __launch_bounds__(128) k_attention_join(const AttnArgs a, int ro
     const AttnSeq s = attn_seq(a, b);
     if (r >= s.n * a.group) return;
     const int64_t total = a.base[a.bt.n_seqs], base = a.base[b];
-    const int nc = attn_chunks(s);
+    const int nc = attn_groups(s);
     const int tok = r / a.group;
     uint16_t *p = a.out + (int64_t)(s.q0 + tok) * a.out_stride + ((int64_t)h * a.group + (r - tok * a.group)) * D +
                   lane * (D / 32);

@@ -135,14 +135,13 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d
 }
 
 template <int D, int NQ>
-cudaError_t launch_tokens(const CUtensorMap &tk, const CUtensorMap &tv, const AttnArgs &a, int ctas, int rows,
-                          cudaStream_t stream, int dev)
+cudaError_t launch_tokens(const AttnArgs &a, int ctas, int rows, cudaStream_t stream, int dev)
 {
     static std::atomic<int> done[kMaxDevices];
     constexpr int smem = at_smem(D, NQ);
     cudaError_t e = ensure_smem(k_attention_tokens<D, NQ>, smem, done, dev);
     if (e == cudaSuccess)
-        e = launch_pdl(k_attention_tokens<D, NQ>, dim3(ctas), dim3((at_warps(NQ) + 1) * 32), smem, stream, tk, tv, a);
+        e = launch_pdl(k_attention_tokens<D, NQ>, dim3(ctas), dim3(at_warps(NQ) * 32), smem, stream, a);
     if (e == cudaSuccess)
         e = launch_pdl(k_attention_join<D>, dim3((unsigned)(a.bt.n_seqs * a.kv.hk), (unsigned)cdiv(rows, 4)),
                        dim3(128), 0, stream, a, 8 * NQ, ctas);
@@ -278,21 +277,20 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
     a.base = reinterpret_cast<int64_t *>(ws);
     a.part_ml = reinterpret_cast<float2 *>(ws + p.base_bytes);
     a.part = reinterpret_cast<float *>(ws + p.base_bytes + p.ml_bytes);
-    CUtensorMap tk, tv;
-    if (!encode_codes(&tk, cache->k, cache->num_pages, hk, cache->page_size, d) ||
-        !encode_codes(&tv, cache->v, cache->num_pages, hk, cache->page_size, d))
-        return BITNET_ERR_CUDA;
     const int ctas = std::min(sms, AT_MAX_CTAS);
     const int rows = a.group * max_new;
     cudaError_t e;
-    if (p.nq == 0)
+    if (p.nq == 0) {
+        CUtensorMap tk, tv;
+        if (!encode_codes(&tk, cache->k, cache->num_pages, hk, cache->page_size, d) ||
+            !encode_codes(&tv, cache->v, cache->num_pages, hk, cache->page_size, d))
+            return BITNET_ERR_CUDA;
         e = d == 128 ? launch_prompt<128>(tk, tv, a, ctas, stream, dev) : launch_prompt<64>(tk, tv, a, ctas, stream, dev);
-    else if (d == 128)
-        e = p.nq == 1 ? launch_tokens<128, 1>(tk, tv, a, ctas, rows, stream, dev)
-                      : launch_tokens<128, 2>(tk, tv, a, ctas, rows, stream, dev);
-    else
-        e = p.nq == 1 ? launch_tokens<64, 1>(tk, tv, a, ctas, rows, stream, dev)
-                      : launch_tokens<64, 2>(tk, tv, a, ctas, rows, stream, dev);
+    } else if (d == 128) {
+        e = p.nq == 1 ? launch_tokens<128, 1>(a, ctas, rows, stream, dev) : launch_tokens<128, 2>(a, ctas, rows, stream, dev);
+    } else {
+        e = p.nq == 1 ? launch_tokens<64, 1>(a, ctas, rows, stream, dev) : launch_tokens<64, 2>(a, ctas, rows, stream, dev);
+    }
     return cuda_status(e);
 }
 
