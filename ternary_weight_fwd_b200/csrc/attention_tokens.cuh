@@ -46,6 +46,13 @@ constexpr int AT_MAX_CTAS = 160;
 constexpr int AT_MIN_UNITS = 16; // groups worth a CTA of their own
 constexpr float AT_LAZY = 8.0f;  // a row's exponents refer to a maximum up to 2^8 behind
 
+// A row tile whose first part is in CTA k's share and the rest in those of the CTAs up to `last`.
+struct AttnShared {
+    int nrow; // 0: CTA k has none
+    int last;
+    int q0, h, r0;
+};
+
 struct AttnArgs {
     KvView kv;
     BatchView bt;
@@ -58,7 +65,8 @@ struct AttnArgs {
     float scale_log2;  // scale * log2(e)
     float *part;       // [2 * CTAs][rows][D] partial sums
     float2 *part_ml;   // [2 * CTAs][rows] their maxima and sums
-    int64_t *base;     // [n_seqs + 1] first unit of each sequence
+    int64_t *base;     // [n_seqs + 1] first unit of each sequence (prompts)
+    AttnShared *shared; // [CTAs] row tiles to join (few tokens)
 };
 
 // Warps for nq tiles of 8 rows: as many as their registers allow (128, 168).
@@ -187,6 +195,12 @@ BITNET_DEVINL int64_t attn_active(int64_t units, int ctas)
     return want < ctas ? want : ctas;
 }
 
+// a / b for a >= 0, b > 0; nearly always both are small.
+BITNET_DEVINL int64_t div_fast(int64_t a, int b)
+{
+    return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Row tiles of `rows` rows per kv head of a sequence, and its units.
 BITNET_DEVINL int attn_row_tiles(const AttnArgs &a, const AttnSeq &s, int rows) { return (s.n * a.group + rows - 1) / rows; }
 BITNET_DEVINL int64_t attn_units(const AttnArgs &a, const AttnSeq &s, int rows)
@@ -282,16 +296,18 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
     }
     const int64_t active = attn_active(total, gridDim.x);
     const bool idle = blockIdx.x >= active;
-    const int64_t c0 = idle ? 0 : total * blockIdx.x / active, c1 = idle ? 0 : total * (blockIdx.x + 1) / active;
-    if (blockIdx.x == 0) { // the join kernel reads the units' bases
-        int64_t at = before;
+    if (blockIdx.x == 0) { // rows of sequences without cached tokens see nothing
         for (int b = b_lo; b < b_hi; ++b) {
-            a.base[b] = at;
-            at += attn_units(a, attn_seq(a, b), ROWS);
+            const AttnSeq s = attn_seq(a, b);
+            if (s.len > 0) continue;
+            for (int t = 0; t < s.n; ++t)
+                for (int x = 0; x < a.kv.hk * a.group * (D / 8); ++x)
+                    reinterpret_cast<uint4 *>(a.out + (int64_t)(s.q0 + t) * a.out_stride)[x] = make_uint4(0, 0, 0, 0);
         }
-        if (tid == 0) a.base[a.bt.n_seqs] = total;
     }
+    if (tid == 0) a.shared[blockIdx.x].nrow = 0; // nothing to join yet
     if (idle) return;
+    const int64_t c0 = div_fast(total * blockIdx.x, (int)active), c1 = div_fast(total * (blockIdx.x + 1), (int)active);
     // where the CTA starts; its warps walk on from there
     int *s_b = reinterpret_cast<int *>(s_step);
     int64_t *s_u = reinterpret_cast<int64_t *>(s_step) + 1;
@@ -327,7 +343,7 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
         if (u >= u1) return;
         ahead.seek(a, u, ROWS);
         const int64_t rel = u - ahead.base;
-        const int ht = (int)(rel / ahead.nc), key0 = (int)(rel - (int64_t)ht * ahead.nc) * AT_GROUP;
+        const int ht = (int)div_fast(rel, ahead.nc), key0 = (int)(rel - (int64_t)ht * ahead.nc) * AT_GROUP;
         const int page = page_of(a.kv, a.bt, ahead.b, key0 >> a.kv.page_shift);
         if (page < 0) return;
         const int64_t at = (int64_t)page * a.kv.hk + ht / ahead.nt;
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
     for (int64_t u = u0; u < u1;) {
         it.seek(a, u, ROWS);
         const int64_t rel = u - it.base;
-        const int ht = (int)(rel / it.nc), t0 = (int)(rel - (int64_t)ht * it.nc);
+        const int ht = (int)div_fast(rel, it.nc), t0 = (int)(rel - (int64_t)ht * it.nc);
         const int h = ht / it.nt, r0 = (ht - h * it.nt) * ROWS; // kv head, first row of the tile
         const int cnt = (int)min((int64_t)(it.nc - t0), u1 - u);
         const int nrow = min(ROWS, it.s.n * a.group - r0);
@@ -677,73 +693,61 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
                 if (lane == 0) a.part_ml[(int64_t)slot * ROWS + r] = make_float2(mm, ll);
             }
         }
+        if (tid == 0 && !whole && pc.first >= c0)
+            a.shared[blockIdx.x] = {pc.nrow, (int)((pc.end * active - 1) / total), pc.q0, pc.h, pc.r0};
         p0 = p1;
     }
 }
 
-// Joins the parts of every row tile (of `rows` rows) that more than one CTA shared,
-// and writes zeros for rows of sequences without cached tokens.  A warp per row;
-// parts are added in the order of the CTAs.
+// Joins the row tiles that more than one CTA shared: block (k, r) row r of the one
+// whose first part CTA k holds.  Four warps take the parts in turn (one warp after
+// another part by part took 19 us for the 30 parts of one long sequence) and are
+// added up in their order.
 template <int D>
-__global__ void __launch_bounds__(128) k_attention_join(const AttnArgs a, int rows, int ctas)
+__global__ void __launch_bounds__(128) k_attention_join(const AttnArgs a, int rows)
 {
+    __shared__ float s_acc[4][D];
+    __shared__ float s_l[4];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.x / a.kv.hk, h = blockIdx.x - b * a.kv.hk;
-    const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const AttnSeq s = attn_seq(a, b);
-    if (r >= s.n * a.group) return;
-    const int64_t total = a.base[a.bt.n_seqs], base = a.base[b];
-    const int nc = attn_groups(s);
-    const int tok = r / a.group;
-    uint16_t *p = a.out + (int64_t)(s.q0 + tok) * a.out_stride + ((int64_t)h * a.group + (r - tok * a.group)) * D +
-                  lane * (D / 32);
-    float acc[D / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.x, r = blockIdx.y;
+    const AttnShared s = a.shared[c0];
+    if (r >= s.nrow) return;
+    auto slot = [&](int k) { return (int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r; };
+    float m = -INFINITY;
+    for (int k = c0 + lane; k <= s.last; k += 32) m = fmaxf(m, a.part_ml[slot(k)].x);
+    m = warp_max(m);
+    float acc[D / 32], l = 0.0f;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
-    float inv = 0.0f;
-    if (nc > 0) {
-        const int64_t active = attn_active(total, ctas);
-        const int64_t ub = base + ((int64_t)h * attn_row_tiles(a, s, rows) + r / rows) * nc, ue = ub + nc - 1;
-        const int c0 = (int)(((ub + 1) * active - 1) / total), c1 = (int)(((ue + 1) * active - 1) / total);
-        if (c0 == c1) return; // one CTA held it whole and wrote the result
-        float m = -INFINITY;
-        for (int k = c0 + lane; k <= c1; k += 32)
-            m = fmaxf(m, a.part_ml[(int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r % rows].x);
-        m = warp_max(m);
-        if (m != -INFINITY) {
-            float l = 0.0f;
-            for (int k0 = c0; k0 <= c1; k0 += 32) {
-                const int k = k0 + lane;
-                float f = 0.0f;
-                if (k <= c1) {
-                    const float2 ml = a.part_ml[(int64_t)(2 * k + (k == c0 ? 1 : 0)) * rows + r % rows];
-                    f = fast_exp2(ml.x - m);
-                    l += ml.y * f;
-                }
-                const int cnt = min(32, c1 - k0 + 1);
-                for (int i = 0; i < cnt; ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i);
-                    const float *src =
-                        a.part + ((int64_t)(2 * (k0 + i) + (k0 + i == c0 ? 1 : 0)) * rows + r % rows) * D + lane * (D / 32);
+    if (m != -INFINITY) {
+#pragma unroll 8
+        for (int k = c0 + warp; k <= s.last; k += 4) {
+            const float2 ml = a.part_ml[slot(k)];
+            const float f = fast_exp2(ml.x - m);
+            const float *src = a.part + slot(k) * D + lane * (D / 32);
+            l += ml.y * f;
 #pragma unroll
-                    for (int e = 0; e < D / 32; ++e) acc[e] += src[e] * fi;
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            inv = 1.0f / l;
+            for (int e = 0; e < D / 32; ++e) acc[e] += src[e] * f;
         }
     }
-    uint32_t w[D / 64];
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-        w[e] = bf16_rn_bits(acc[2 * e] * inv) | (bf16_rn_bits(acc[2 * e + 1] * inv) << 16);
-    if constexpr (D == 128)
-        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-    else
-        *reinterpret_cast<uint32_t *>(p) = w[0];
+    for (int e = 0; e < D / 32; ++e) s_acc[warp][lane * (D / 32) + e] = acc[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int d = 2 * threadIdx.x + e;
+        x[e] = ((s_acc[0][d] + s_acc[1][d]) + (s_acc[2][d] + s_acc[3][d])) * inv;
+    }
+    const int tok = (s.r0 + r) / a.group;
+    reinterpret_cast<uint32_t *>(a.out + (int64_t)(s.q0 + tok) * a.out_stride +
+                                 ((int64_t)s.h * a.group + (s.r0 + r - tok * a.group)) * D)[threadIdx.x] =
+        bf16_rn_bits(x[0]) | (bf16_rn_bits(x[1]) << 16);
 }
 
 } // namespace bitnet

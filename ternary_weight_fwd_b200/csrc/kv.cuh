@@ -114,7 +114,7 @@ bool encode_queries(CUtensorMap *map, const void *q, int64_t T, int64_t stride, 
 struct AttnPlan {
     bool ok;
     int nq; // tiles of 8 rows of the kernel for few tokens (1 or 2); 0: the kernel for prompts
-    size_t base_bytes, ml_bytes, part_bytes;
+    size_t base_bytes, ml_bytes, part_bytes; // units' bases or shared row tiles; parts' maxima and sums; parts
     size_t total() const { return base_bytes + ml_bytes + part_bytes; }
 };
 
@@ -127,7 +127,7 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d
     const int64_t rows = n_heads / hk * max_new;
     p.nq = rows <= 8 ? 1 : rows <= AT_MAX_ROWS ? 2 : 0;
     const size_t part_rows = (size_t)2 * AT_MAX_CTAS * (p.nq ? 8 * p.nq : AP_ROWS);
-    p.base_bytes = align_up((size_t)(n_seqs + 1) * 8, 256);
+    p.base_bytes = p.nq ? align_up(AT_MAX_CTAS * sizeof(AttnShared), 256) : align_up((size_t)(n_seqs + 1) * 8, 256);
     p.ml_bytes = align_up(part_rows * sizeof(float2), 256);
     p.part_bytes = part_rows * d * sizeof(float);
     p.ok = true;
@@ -143,8 +143,8 @@ cudaError_t launch_tokens(const AttnArgs &a, int ctas, int rows, cudaStream_t st
     if (e == cudaSuccess)
         e = launch_pdl(k_attention_tokens<D, NQ>, dim3(ctas), dim3(at_warps(NQ) * 32), smem, stream, a);
     if (e == cudaSuccess)
-        e = launch_pdl(k_attention_join<D>, dim3((unsigned)(a.bt.n_seqs * a.kv.hk), (unsigned)cdiv(rows, 4)),
-                       dim3(128), 0, stream, a, 8 * NQ, ctas);
+        e = launch_pdl(k_attention_join<D>, dim3(ctas, (unsigned)std::min(rows, 8 * NQ)), dim3(128), 0,
+                       stream, a, 8 * NQ);
     return e;
 }
 
@@ -275,6 +275,7 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
     a.scale_log2 = scale * 1.44269504088896341f;
     char *ws = static_cast<char *>(workspace);
     a.base = reinterpret_cast<int64_t *>(ws);
+    a.shared = reinterpret_cast<AttnShared *>(ws);
     a.part_ml = reinterpret_cast<float2 *>(ws + p.base_bytes);
     a.part = reinterpret_cast<float *>(ws + p.base_bytes + p.ml_bytes);
     const int ctas = std::min(sms, AT_MAX_CTAS);
