@@ -10,8 +10,8 @@
 // (sequence, kv head, tile of 8 or 16 rows, group of 16 tokens) in that order,
 // cut into equal contiguous shares, one per CTA (one CTA per SM), and those into
 // equal shares per warp, so ragged batches and single long sequences load every
-// SM alike.  A warp works alone: it copies its groups' codes into its own two
-// buffers in shared memory, the next while it computes on one, keeps its own
+// SM alike.  A warp works alone: it copies its groups' codes into its own
+// buffers in shared memory, the next ones while it computes on one, keeps its own
 // running maxima and sums, and waits for no other warp before the end.  Then the
 // CTA adds up the pieces of (sequence, kv head, row tile) that its warps share, in
 // the order of the warps; what it shares with other CTAs (at most two) goes to the
@@ -69,12 +69,15 @@ struct AttnArgs {
     AttnShared *shared; // [CTAs] row tiles to join (few tokens)
 };
 
-// Warps for nq tiles of 8 rows: as many as their registers allow (128, 168).
-constexpr __host__ __device__ int at_warps(int nq) { return nq == 1 ? 16 : 12; }
+// Warps for nq tiles of 8 rows: as many as leave each the registers it wants (168, 255).
+// With 16 and 12 warps of 128 and 168: 52 us instead of 47 (64 sequences), 64 instead of 48
+// (16 sequences of four new tokens, 8 query heads a kv head).
+constexpr __host__ __device__ int at_warps(int nq) { return nq == 1 ? 12 : 8; }
+constexpr int AT_BUFS = 2; // a warp's buffers of a group's codes (three: no faster)
 
 constexpr __host__ __device__ int at_smem(int d, int nq)
 {
-    return 4096 + at_warps(nq) * (2 * 2 * AT_GROUP * d + 8 * nq * (d + 4) * 4 + 2 * 8 * nq * 8) + 1024;
+    return 4096 + at_warps(nq) * (AT_BUFS * 2 * AT_GROUP * d + 8 * nq * (d + 4) * 4 + 2 * 8 * nq * 8) + 1024;
 }
 
 // 3-D tiled tensor copy global -> shared (no multicast); c0 is 0 here.
@@ -264,11 +267,11 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int64_t *s_scan = reinterpret_cast<int64_t *>(smem);            // [WARPS] sums
     AtPiece *s_piece = reinterpret_cast<AtPiece *>(smem + 256);     // [WARPS][2]
-    float2 *s_step = reinterpret_cast<float2 *>(smem + 256 + 32 * 32 + 256); // [WARPS][2 buffers] k_step, v_step
-    unsigned char *ring = smem + 4096;                              // [WARPS][2 buffers][K, V]
-    float *s_first = reinterpret_cast<float *>(ring + WARPS * 4 * TILE); // [WARPS][ROWS][PROW]: first pieces
+    float2 *s_step = reinterpret_cast<float2 *>(smem + 256 + 32 * 32 + 256); // [WARPS][buffers] k_step, v_step
+    unsigned char *ring = smem + 4096;                              // [WARPS][buffers][K, V]
+    float *s_first = reinterpret_cast<float *>(ring + WARPS * AT_BUFS * 2 * TILE); // [WARPS][ROWS][PROW]: first pieces
     float2 *s_ml = reinterpret_cast<float2 *>(s_first + WARPS * ROWS * PROW); // [WARPS][2][ROWS]
-    static_assert(WARPS <= 16 && sizeof(AtPiece) == 32 && 256 + 1024 + 256 + 16 * 2 * 8 <= 4096, "layout");
+    static_assert(WARPS <= 16 && sizeof(AtPiece) == 32 && 256 + 1024 + 256 + 16 * AT_BUFS * 8 <= 4096, "layout");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
@@ -331,8 +334,8 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
     __syncthreads(); // s_step is the warps' own from here on
 
     const int64_t u0 = c0 + (c1 - c0) * warp / WARPS, u1 = c0 + (c1 - c0) * (warp + 1) / WARPS;
-    const uint32_t ring_base = smem_u32(ring) + warp * 4 * TILE;
-    float2 *steps = s_step + warp * 2;
+    const uint32_t ring_base = smem_u32(ring) + warp * AT_BUFS * 2 * TILE;
+    float2 *steps = s_step + warp * AT_BUFS;
 
     // ---- copies ----
     // 32 groups at a time, a lane looks up a group's page and steps, one such batch ahead.
@@ -355,9 +358,9 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
     float ks_a, vs_a, ks_b, vs_b;
     look_up(u0 + lane, row_a, ks_a, vs_a);
     look_up(u0 + 32 + lane, row_b, ks_b, vs_b);
-    int issued = 0; // groups whose copies are under way or done
+    int issued = 0, buf = 0; // groups whose copies are under way or done, the next one's buffer
     auto copy = [&]() {
-        const int from = issued & 31, buf = issued & 1;
+        const int from = issued & 31;
         const int64_t row = __shfl_sync(0xffffffffu, row_a, from);
         const float ks = __shfl_sync(0xffffffffu, ks_a, from), vs = __shfl_sync(0xffffffffu, vs_a, from);
         if (row >= 0) {
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
         }
         if (lane == 0) steps[buf] = make_float2(ks, vs);
         asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++buf == AT_BUFS) buf = 0;
         ++issued;
         if ((issued & 31) == 0) {
             row_a = row_b;
@@ -381,13 +385,13 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
             look_up(u0 + issued + 32 + lane, row_b, ks_b, vs_b);
         }
     };
-    copy();
-    copy();
+#pragma unroll 1
+    for (int i = 0; i < AT_BUFS; ++i) copy();
 
     const int g = lane >> 2, c = lane & 3;
     const int key_g = (g & 1) ? ((g + 4) & 7) : g;      // token of score row g (g + 8: + 8): 0 5 2 7 4 1 6 3, see below
     const int key_e = 2 * c, key_o = (2 * c + 5) & 7;   // tokens of contraction indices 2c, 2c + 1 of the second product
-    int done = 0; // groups consumed
+    int use = 0; // buffer of the next group
 
     for (int64_t u = u0; u < u1;) {
         it.seek(a, u, ROWS);
@@ -448,13 +452,13 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
         float unit = 0.0f, inv_unit = 0.0f; // o is in units of this power of two; 0: not chosen yet
 
         for (int i = 0; i < cnt; ++i) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory"); // all but the newest copies
+            asm volatile("cp.async.wait_group %0;" ::"n"(AT_BUFS - 1) : "memory"); // the oldest copies have landed
             __syncwarp();
             const int key0 = (t0 + i) * AT_GROUP;
             {
-                const float2 step = steps[done & 1];
+                const float2 step = steps[use];
                 const float ks = step.x, vs = step.y;
-                const uint32_t kb = ring_base + (done & 1) * 2 * TILE, vb = kb + TILE;
+                const uint32_t kb = ring_base + use * 2 * TILE, vb = kb + TILE;
                 float s[NQ][4];
 #pragma unroll
                 for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
             }
             __syncwarp(); // the buffer has been read
             copy();
-            ++done;
+            if (++use == AT_BUFS) use = 0;
         }
 
         // ---- sums of the lanes; the piece or the result ----
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
             const int k = u == u0 ? 0 : 1;
             if (k) asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-            float *dst = k ? reinterpret_cast<float *>(ring + warp * 4 * TILE) : s_first + warp * ROWS * PROW;
+            float *dst = k ? reinterpret_cast<float *>(ring + warp * AT_BUFS * 2 * TILE) : s_first + warp * ROWS * PROW;
             const int prow = k ? D : PROW;
 #pragma unroll
             for (int t = 0; t < NQ; ++t)
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
                     if (s_piece[p].first < 0) continue;
                     const float2 ml = s_ml[p * ROWS + r];
                     const float f = fast_exp2(ml.x - mm);
-                    const float *src = (p & 1) ? reinterpret_cast<const float *>(ring + (p >> 1) * 4 * TILE) + r * D
+                    const float *src = (p & 1) ? reinterpret_cast<const float *>(ring + (p >> 1) * AT_BUFS * 2 * TILE) + r * D
                                                : s_first + (p >> 1) * ROWS * PROW + r * PROW;
                     ll += ml.y * f;
 #pragma unroll
