@@ -224,7 +224,8 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
     a.q_out = static_cast<uint16_t *>(q_out);
     a.q_out_stride = q_out_stride;
     a.group = q ? n_heads / hk : 0;
-    const dim3 grid((unsigned)ka_base(a.bt.T, a.bt.n_seqs, a.kv.page_shift), (unsigned)hk, 2);
+    const int heads = KA_WARPS >> (a.kv.page_shift - 4); // kv heads per CTA
+    const dim3 grid((unsigned)ka_base(a.bt.T, a.bt.n_seqs, a.kv.page_shift), (unsigned)cdiv(hk, heads), 2);
     const bool f32 = dtype == BITNET_DTYPE_F32;
     cudaError_t e;
     if (d == 128)
