@@ -73,11 +73,12 @@ bool rows_share(const void *a, int64_t sa, int64_t wa, const void *b, int64_t sb
 template <bool F32, int D>
 cudaError_t launch_append(const AppendArgs &a, int page_shift, dim3 grid, cudaStream_t stream)
 {
+    const dim3 block(ka_warps(page_shift) * 32);
     switch (page_shift) {
-    case 4: return launch_pdl(k_kv_append<F32, D, 16>, grid, dim3(KA_THREADS), 0, stream, a);
-    case 5: return launch_pdl(k_kv_append<F32, D, 32>, grid, dim3(KA_THREADS), 0, stream, a);
-    case 6: return launch_pdl(k_kv_append<F32, D, 64>, grid, dim3(KA_THREADS), 0, stream, a);
-    default: return launch_pdl(k_kv_append<F32, D, 128>, grid, dim3(KA_THREADS), 0, stream, a);
+    case 4: return launch_pdl(k_kv_append<F32, D, 16>, grid, block, 0, stream, a);
+    case 5: return launch_pdl(k_kv_append<F32, D, 32>, grid, block, 0, stream, a);
+    case 6: return launch_pdl(k_kv_append<F32, D, 64>, grid, block, 0, stream, a);
+    default: return launch_pdl(k_kv_append<F32, D, 128>, grid, block, 0, stream, a);
     }
 }
 
@@ -224,7 +225,7 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
     a.q_out = static_cast<uint16_t *>(q_out);
     a.q_out_stride = q_out_stride;
     a.group = q ? n_heads / hk : 0;
-    const int heads = KA_WARPS >> (a.kv.page_shift - 4); // kv heads per CTA
+    const int heads = ka_warps(a.kv.page_shift) >> (a.kv.page_shift - 4); // kv heads per CTA
     const dim3 grid((unsigned)ka_base(a.bt.T, a.bt.n_seqs, a.kv.page_shift), (unsigned)cdiv(hk, heads), 2);
     const bool f32 = dtype == BITNET_DTYPE_F32;
     cudaError_t e;

@@ -5,11 +5,11 @@
 // decides it meets in one team of warps (one warp per 16 tokens of a page): the rows
 // are read once, stay in registers across the maximum, and codes and step are
 // written by the same threads.  No atomics and no second pass over q, k, v.  A CTA
-// of eight warps holds as many teams, for neighbouring kv heads, as fit (a CTA per
+// holds as many teams, for neighbouring kv heads, as fit (a CTA per
 // 16-token page and head spent its time on being launched: 145 us for 17 k tokens
 // of 16 heads, against 43 us for the bytes).  The team of a key also rotates the
 // query heads of its group for the same tokens: they need the same row lookup, and
-// the cosines and sines, twice a bf16 row's bytes, stay in registers for them.
+// the cosines and sines, twice a bf16 row's bytes, serve all of them from registers.
 //
 // Bound by HBM: q, k, v are read once, rotated queries and codes written once.
 #pragma once
@@ -18,8 +18,9 @@
 
 namespace bitnet {
 
-constexpr int KA_THREADS = 256;
-constexpr int KA_WARPS = KA_THREADS / 32;
+// Warps per CTA for pages of 2^shift tokens: a page of 128 needs a team of eight, and
+// small CTAs share the SMs more evenly.
+constexpr __host__ __device__ int ka_warps(int page_shift) { return page_shift == 7 ? 8 : 4; }
 
 struct AppendArgs {
     KvView kv;
@@ -43,32 +44,44 @@ __host__ BITNET_DEVINL int64_t ka_base(int64_t q0, int64_t b, int page_shift)
     return q0 < byp ? q0 : byp;
 }
 
-// Sixteen elements of a row: x[0..7] at j, x[8..15] at j + D / 2.
+// Sixteen elements of a row as they lie in memory: eight at elem, eight at elem + D / 2.
 template <bool F32, int D>
-BITNET_DEVINL void ka_load(const void *base, int64_t elem, float (&x)[16])
+BITNET_DEVINL void ka_raw(const void *base, int64_t elem, uint4 (&w)[F32 ? 4 : 2])
 {
+    constexpr int size = F32 ? 4 : 2;
+    const char *p = static_cast<const char *>(base) + elem * size;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if constexpr (F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem + h * (D / 2));
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 v = p[i];
-                x[8 * h + 4 * i] = v.x;
-                x[8 * h + 4 * i + 1] = v.y;
-                x[8 * h + 4 * i + 2] = v.z;
-                x[8 * h + 4 * i + 3] = v.w;
-            }
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + elem + h * (D / 2));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < size / 2; ++i)
+            w[h * (size / 2) + i] = reinterpret_cast<const uint4 *>(p + h * (D / 2) * size)[i];
+}
+
+template <bool F32>
+BITNET_DEVINL void ka_values(const uint4 (&w)[F32 ? 4 : 2], float (&x)[16])
+{
+    constexpr int N = F32 ? 4 : 8; // elements of a 16-byte chunk
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[8 * h + 2 * i] = bf16_bits_lo(w[i]);
-                x[8 * h + 2 * i + 1] = bf16_bits_hi(w[i]);
+    for (int i = 0; i < 16 / N; ++i) {
+        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (F32) {
+                x[N * i + e] = __uint_as_float(v[e]);
+            } else {
+                x[N * i + 2 * e] = bf16_bits_lo(v[e]);
+                x[N * i + 2 * e + 1] = bf16_bits_hi(v[e]);
             }
         }
     }
+}
+
+template <bool F32, int D>
+BITNET_DEVINL void ka_load(const void *base, int64_t elem, float (&x)[16])
+{
+    uint4 w[F32 ? 4 : 2];
+    ka_raw<F32, D>(base, elem, w);
+    ka_values<F32>(w, x);
 }
 
 BITNET_DEVINL void ka_load8(const float *p, float (&x)[8])
@@ -100,10 +113,44 @@ BITNET_DEVINL int ka_code(float x, float step)
     return max(-127, min(127, c));
 }
 
+// Codes of sixteen elements, rne(fl(x / step)) each, four to a word.  x times the rounded
+// inverse is within 127 * 3 * 2^-24 < 3e-5 of fl(x / step), so where it is not within 1e-4
+// of the middle between two integers both round alike; else (one set of sixteen in 300), and
+// for steps near the subnormal ones, the division itself decides.  (Dividing always: 81 us
+// for 17 k tokens of 16 heads, the divisions' units 35 % busy.)
+BITNET_DEVINL void ka_codes(const float (&x)[16], float step, float inv, uint32_t (&w)[4])
+{
+    constexpr float magic = 12582912.0f; // 1.5 * 2^23: the sum's low byte is the nearest integer
+    bool exact = step < 1e-30f;
+    if (!exact) {
+        float off = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t n[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float t = __fmul_rn(x[4 * i + e], inv), r = __fadd_rn(t, magic);
+                off = fmaxf(off, fabsf(__fsub_rn(t, __fsub_rn(r, magic))));
+                n[e] = __float_as_uint(r);
+            }
+            w[i] = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+        }
+        exact = off > 0.4999f;
+    }
+    if (exact) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack4_s8(ka_code(x[4 * i], step), ka_code(x[4 * i + 1], step), ka_code(x[4 * i + 2], step),
+                            ka_code(x[4 * i + 3], step));
+    }
+}
+
 // D: head dimension; P: page size.
 template <bool F32, int D, int P>
-__global__ void __launch_bounds__(KA_THREADS) k_kv_append(const AppendArgs a)
+__global__ void __launch_bounds__(P == 128 ? 256 : 128, (D == 64 ? 6 : 4) / (P == 128 ? 2 : 1))
+    k_kv_append(const AppendArgs a)
 {
+    constexpr int KA_WARPS = P == 128 ? 8 : 4, KA_THREADS = KA_WARPS * 32;
     constexpr int TEAM = P / 16;             // warps per (page, kv head)
     constexpr int LPR = D / 16;              // lanes per row, sixteen elements each
     constexpr int RPP = 32 / LPR;            // rows a warp holds side by side
@@ -149,7 +196,42 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv_append(const AppendArgs a)
     const int col = (lane % LPR) * 8;
     const int r0 = (warp % TEAM) * 16 + lane / LPR; // this thread's rows: r0, r0 + RPP, ...
 
-    // keys or values, rotated, kept; queries of the key's group on the way
+    // queries of the key's group: several heads' loads at a time, or each waits for the one before
+    if (is_k && mine && a.group > 0) {
+        constexpr int CH = F32 ? 2 : 4;
+#pragma unroll 1
+        for (int r = r0; r < min(nn, r0 + 16); r += RPP) {
+            float c[8], s[8];
+            if (a.rope) {
+                const float *rope = a.rope + (int64_t)(lo + r) * D + col;
+                ka_load8(rope, c);
+                ka_load8(rope + D / 2, s);
+            }
+            const int64_t q = (row0 + r) * a.q_stride + (int64_t)h * a.group * D + col;
+            uint16_t *out = a.q_out + (row0 + r) * a.q_out_stride + (int64_t)h * a.group * D + col;
+#pragma unroll 1
+            for (int g0 = 0; g0 < a.group; g0 += CH) {
+                uint4 raw[CH][F32 ? 4 : 2];
+#pragma unroll
+                for (int g = 0; g < CH; ++g)
+                    if (g0 + g < a.group) ka_raw<F32, D>(a.q, q + (g0 + g) * D, raw[g]);
+#pragma unroll
+                for (int g = 0; g < CH; ++g) {
+                    if (g0 + g >= a.group) break;
+                    float y[16];
+                    ka_values<F32>(raw[g], y);
+                    if (a.rope) ka_rotate(c, s, y);
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = bf16_rn_bits(y[2 * e]) | (bf16_rn_bits(y[2 * e + 1]) << 16);
+                    *reinterpret_cast<uint4 *>(out + (g0 + g) * D) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(out + (g0 + g) * D + D / 2) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+        }
+    }
+
+    // keys or values, rotated, kept until the page's maximum is known
     const void *src = is_k ? a.k : a.v;
     const int64_t stride = is_k ? a.k_stride : a.v_stride;
     float x[NR][16];
@@ -161,31 +243,16 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv_append(const AppendArgs a)
         for (int e = 0; e < 16; ++e) x[i][e] = 0.0f;
         if (mine && r < nn) ka_load<F32, D>(src, (row0 + r) * stride + (int64_t)h * D + col, x[i]);
     }
-    if (is_k && mine) {
+    if (is_k && mine && a.rope) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int r = r0 + i * RPP;
             if (r >= nn) continue;
             float c[8], s[8];
-            if (a.rope) {
-                const float *rope = a.rope + (int64_t)(lo + r) * D + col;
-                ka_load8(rope, c);
-                ka_load8(rope + D / 2, s);
-                ka_rotate(c, s, x[i]);
-            }
-            const int64_t q = (row0 + r) * a.q_stride + (int64_t)h * a.group * D + col;
-            uint16_t *out = a.q_out + (row0 + r) * a.q_out_stride + (int64_t)h * a.group * D + col;
-#pragma unroll 2
-            for (int g = 0; g < a.group; ++g) {
-                float y[16];
-                ka_load<F32, D>(a.q, q + g * D, y);
-                if (a.rope) ka_rotate(c, s, y);
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = bf16_rn_bits(y[2 * e]) | (bf16_rn_bits(y[2 * e + 1]) << 16);
-                *reinterpret_cast<uint4 *>(out + g * D) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(out + g * D + D / 2) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+            const float *rope = a.rope + (int64_t)(lo + r) * D + col;
+            ka_load8(rope, c);
+            ka_load8(rope + D / 2, s);
+            ka_rotate(c, s, x[i]);
         }
     }
 #pragma unroll
@@ -207,6 +274,7 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv_append(const AppendArgs a)
     if (!write) return;
     int8_t *codes = (is_k ? a.kv.k : a.kv.v) + head * P * D;
     const float step = fmaxf(old, __fmul_rn(mx, 1.0f / 127.0f));
+    const float inv = __frcp_rn(step);
     const int tl = tid % (TEAM * 32); // thread of the team
     if (step > old) {
         __syncwarp();
@@ -233,12 +301,7 @@ __global__ void __launch_bounds__(KA_THREADS) k_kv_append(const AppendArgs a)
         const int r = r0 + i * RPP;
         if (r >= nn) continue;
         uint32_t w[4] = {0, 0, 0, 0};
-        if (step > 0.0f) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = pack4_s8(ka_code(x[i][4 * e], step), ka_code(x[i][4 * e + 1], step),
-                                ka_code(x[i][4 * e + 2], step), ka_code(x[i][4 * e + 3], step));
-        }
+        if (step > 0.0f) ka_codes(x[i], step, inv, w);
         int8_t *dst = codes + (off + r) * D + col;
         *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2 *>(dst + D / 2) = make_uint2(w[2], w[3]);
