@@ -471,6 +471,27 @@ def kv_cache(num_pages: int, n_kv_heads: int, head_dim: int, page_size: int, dev
 def _kv_views(cache, page_table, seq_lens, q_start, rows):
     """The C structs of a cache and a batch, after the checks that need the tensors."""
     k, v, k_step, v_step = cache
+    dev = k.get_device()
+    shape = k.shape
+    n = seq_lens.numel()
+    if not (dev >= 0 and len(shape) == 4 and v.shape == shape and k_step.shape == shape[:2]
+            and v_step.shape == shape[:2] and page_table.dim() == 2 and page_table.shape[0] == n
+            and q_start.numel() == n + 1
+            and k.dtype is v.dtype is torch.int8 and k_step.dtype is v_step.dtype is torch.float32
+            and page_table.dtype is seq_lens.dtype is q_start.dtype is torch.int32
+            and v.get_device() == k_step.get_device() == v_step.get_device() == page_table.get_device()
+            == seq_lens.get_device() == q_start.get_device() == dev
+            and k.is_contiguous() and v.is_contiguous() and k_step.is_contiguous() and v_step.is_contiguous()
+            and page_table.is_contiguous() and seq_lens.is_contiguous() and q_start.is_contiguous()):
+        _kv_refuse(cache, page_table, seq_lens, q_start)
+    return (bitnet_kv_cache_t(k.data_ptr(), v.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), *shape),
+            bitnet_kv_batch_t(page_table.data_ptr(), seq_lens.data_ptr(), q_start.data_ptr(), page_table.shape[1], n,
+                              rows))
+
+
+def _kv_refuse(cache, page_table, seq_lens, q_start):
+    """Say what is wrong with a cache and a batch."""
+    k, v, k_step, v_step = cache
     dev = k.device
     for t, dt, name in ((k, torch.int8, "k"), (v, torch.int8, "v"), (k_step, torch.float32, "k_step"),
                         (v_step, torch.float32, "v_step"), (page_table, torch.int32, "page_table"),
@@ -481,50 +502,47 @@ def _kv_views(cache, page_table, seq_lens, q_start, rows):
             raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda:
+    if not k.is_cuda:
         raise ValueError(f"the cache is on {dev}, not on a GPU")
-    pages, hk, size, d = k.shape
-    n = seq_lens.numel()
-    if v.shape != k.shape or k_step.shape != (pages, hk) or v_step.shape != (pages, hk):
-        raise ValueError("k, v and their steps do not belong together")
-    if page_table.dim() != 2 or page_table.shape[0] != n or q_start.numel() != n + 1:
-        raise ValueError("page_table, seq_lens and q_start must describe the same sequences")
-    return (bitnet_kv_cache_t(k.data_ptr(), v.data_ptr(), k_step.data_ptr(), v_step.data_ptr(), pages, hk, size, d),
-            bitnet_kv_batch_t(page_table.data_ptr(), seq_lens.data_ptr(), q_start.data_ptr(), page_table.shape[1], n,
-                              rows))
+    if k.dim() != 4 or v.shape != k.shape or k_step.shape != k.shape[:2] or v_step.shape != k.shape[:2]:
+        raise ValueError("k, v [pages][kv heads][page size][head dim] and their steps [pages][kv heads] do not fit")
+    raise ValueError("page_table, seq_lens and q_start must describe the same sequences")
 
 
 def _kv_rows(t, name, like, heads, dtype=None):
     """Row stride of [T][heads][head dim] rows whose heads are contiguous."""
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     d = like.shape[3]
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [T][{heads or 'heads'}][{d}], got {tuple(t.shape)}")
-    if t.device != like.device:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [T][{heads or 'heads'}][{d}], got {tuple(shape)}")
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != d):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+    return stride[0] if shape[0] > 1 else shape[1] * d
 
 
-def _kv_call(name, dev, stream, made, *args):
-    """Call a C entry on the tensors' device and the given (or that device's current) stream; memory
-    made for the call is kept from reuse until the stream is through with it."""
+def _kv_call(name, index, stream, made, *args):
+    """Call a C entry on device `index` and the given (or that device's current) stream; memory made for
+    the call is kept from reuse until the stream is through with it."""
     fn = getattr(load_library(), name)
     if stream is None:
-        s = torch.cuda.current_stream(dev)
+        raw = torch._C._cuda_getCurrentRawStream(index)  # torch.cuda.current_stream(index).cuda_stream, 2 us faster
     else:
-        s = stream
-        if s.device != dev:
-            raise ValueError(f"{name}: the stream is on {s.device}, the cache on {dev}")
+        if stream.device.index != index:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{index}")
+        raw = stream.cuda_stream
         for t in made:
-            t.record_stream(s)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, s.cuda_stream), name)
+            t.record_stream(stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, s.cuda_stream), name)
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != BITNET_OK:
+        raise BitnetError(status, name)
 
 
 def bitnet_rope_table(max_pos, head_dim, theta=ROPE_THETA, *, table=None, device="cuda", stream=None):
@@ -537,7 +555,7 @@ def bitnet_rope_table(max_pos, head_dim, theta=ROPE_THETA, *, table=None, device
         raise ValueError(f"table must be contiguous fp32 [{max_pos}][{head_dim}]")
     if not table.is_cuda:
         raise ValueError(f"table is on {table.device}, not on a GPU")
-    _kv_call("bitnet_rope_table", table.device, stream, made, float(theta), max_pos, head_dim, table.data_ptr())
+    _kv_call("bitnet_rope_table", table.device.index, stream, made, float(theta), max_pos, head_dim, table.data_ptr())
     return table
 
 
@@ -573,10 +591,11 @@ def bitnet_kv_append(cache, page_table, seq_lens, q_start, k, v, *, q=None, rope
     if rope is not None:
         if rope.dtype != torch.float32:
             raise TypeError(f"rope must be float32, got {rope.dtype}")
-        if rope.dim() != 2 or rope.shape[1] != kc.shape[3] or not rope.is_contiguous() or rope.device != kc.device:
+        if (rope.dim() != 2 or rope.shape[1] != kc.shape[3] or not rope.is_contiguous()
+                or rope.get_device() != kc.get_device()):
             raise ValueError(f"rope must be contiguous [positions][{kc.shape[3]}] on {kc.device}")
         rp, rope_len = rope.data_ptr(), rope.shape[0]
-    _kv_call("bitnet_kv_append", kc.device, stream, made, c, b, qp, k.data_ptr(), v.data_ptr(), _dtype_code(k), heads,
+    _kv_call("bitnet_kv_append", kc.get_device(), stream, made, c, b, qp, k.data_ptr(), v.data_ptr(), _dtype_code(k), heads,
              qs, ks, vs, rp, rope_len, op, os_)
     return q_out
 
@@ -606,9 +625,9 @@ def bitnet_attention(cache, page_table, seq_lens, q_start, q, max_new, *, scale=
         need = load_library().bitnet_attention_workspace_size(b.n_seqs, rows, heads, c.n_kv_heads, d, max_new)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         made += (workspace,)
-    elif workspace.device != q.device:
+    elif workspace.get_device() != q.get_device():
         raise ValueError(f"workspace is on {workspace.device}, the cache on {q.device}")
-    _kv_call("bitnet_attention", kc.device, stream, made, c, b, q.data_ptr(), qs, heads, max_new,
+    _kv_call("bitnet_attention", kc.get_device(), stream, made, c, b, q.data_ptr(), qs, heads, max_new,
              d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
              workspace.numel() * workspace.element_size())
     return out
