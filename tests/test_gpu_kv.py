@@ -291,3 +291,236 @@ def test_prompt_same_bits_every_time():
     a = check_attention(b, cache, 12, 128, 191)
     for _ in range(3):
         assert same_bits(a, check_attention(b, cache, 12, 128, 191))
+
+
+# ---- calls as they are used: together, captured, on streams, refused on the device -----------------------
+def layer_inputs(seed, hq=4, hk=2, d=64, width=256):
+    from gpu_util import make_weights
+    return {n: make_weights(o, i, seed + k) for k, (n, o, i) in
+            enumerate((("q", hq * d, width), ("k", hk * d, width), ("v", hk * d, width), ("o", width, hq * d)))}
+
+
+def test_decoder_attention_run():
+    """A prompt and three decode steps of one layer's attention as a user chains it: BitLinear q, k, v,
+    append, attention, output BitLinear.  Every stage is checked on what the stage before really gave."""
+    import oracle
+    from gpu_util import assert_rel_close, make_x
+    hq, hk, d, page, width = 4, 2, 64, 16, 256
+    W = layer_inputs(500, hq, hk, d, width)
+    rope = tw.bitnet_rope_table(256, d)
+    tab = rope.cpu().numpy()
+    cache = tw.kv_cache(12, hk, d, page)
+    ref = [x.cpu().numpy() for x in cache]
+    table = np.array([[7, 2, 9, 0], [4, 11, 1, 5]], np.int32)
+    lens = np.zeros(2, np.int32)
+    for step, new in enumerate([(37, 20), (1, 1), (1, 3), (2, 0)]):
+        t = sum(new)
+        lens = lens + np.array(new, np.int32)
+        starts = np.array([0, new[0], t], np.int32)
+        x, xf = make_x(t, width, 510 + step)
+        q, k, v = (tw.bitnet_linear_ex(x, W[n]["p"], W[n]["g"], y_dtype=torch.bfloat16).view(t, -1, d)
+                   for n in ("q", "k", "v"))
+        qr = tw.bitnet_kv_append(cache, dev(table), dev(lens), dev(starts), k, v, q=q, rope=rope)
+        out = tw.bitnet_attention(cache, dev(table), dev(lens), dev(starts), qr, max(new))
+        y = tw.bitnet_linear_norm(out.view(t, -1), torch.ones(hq * d, device=DEV), W["o"]["p"], W["o"]["g"])
+        torch.cuda.synchronize()
+        host = [z.float().cpu().numpy() for z in (q, k, v)]
+        want = kv_ref.append(ref, table, lens, starts, host[1], host[2], host[0], tab)
+        assert all(same_bits(a.cpu().numpy(), b) for a, b in zip(cache, ref))
+        assert same_bits(qr.float().cpu().numpy(), want)
+        o = out.float().cpu().numpy()
+        exact = kv_ref.attention(ref, table, lens, starts, want)
+        assert (np.abs(o - exact) <= kv_ref.attention_bound(ref, table, lens, starts, want, exact)).all()
+        y_ref = oracle.bitlinear_norm(o.reshape(t, -1), np.ones(hq * d, np.float32), W["o"]["p_ref"], W["o"]["g_ref"],
+                                      hq * d)[0]
+        assert_rel_close(y.cpu().numpy(), y_ref)
+
+
+def batch_on_device(b):
+    return dev(b["table"]), dev(b["lens"]), dev(b["q_start"])
+
+
+@pytest.mark.parametrize("new,max_new", [([1, 1, 1, 0], 1), ([70, 1, 33, 2], 70)])
+def test_captured_and_replayed(new, max_new):
+    """Append and attention captured once and replayed with other lengths, pages and values in the same
+    buffers; a second graph shares the workspace, replayed in turn."""
+    hq, hk, d, page = 8, 2, 128, 32
+    lens = [130, 1, 40, 9]
+    a = make_batch(new, lens, page, 601, width=8)
+    b = make_batch(new[::-1], [n + 50 for n in new[::-1]], page, 602, width=8, spare=2)
+    t = a["rows"]
+    assert b["rows"] == t
+    pages = max(a["pages"], b["pages"])
+    caches = [make_cache(pages, hk, page, d, 603 + i) for i in range(2)]
+    state = [torch.zeros_like(x) for x in to_dev(caches[0])]
+    table, seq, starts = (torch.zeros_like(x) for x in batch_on_device(a))
+    x = [rows((t, n, d), 610 + i) for i, n in enumerate((hq, hk, hk))]
+    y = [rows((t, n, d), 620 + i) for i, n in enumerate((hq, hk, hk))]
+    q, k, v = (z[0].clone() for z in x)
+    rope_np = kv_ref.rope_table(256, d)
+    rope = dev(rope_np)
+    need = tw.bitnet_attention_workspace_size(4, t, hq, hk, d, max_new)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV)
+    outs = [torch.zeros((t, hq, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    qr = torch.zeros((t, hq, d), dtype=torch.bfloat16, device=DEV)
+    graphs = []
+    for out in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tw.bitnet_kv_append(state, table, seq, starts, k, v, q=q, rope=rope, q_out=qr)
+            tw.bitnet_attention(state, table, seq, starts, qr, max_new, out=out, workspace=ws)
+        graphs.append(g)
+    for turn, (bt, cache, z) in enumerate(((a, caches[0], x), (b, caches[1], y), (a, caches[1], y))):
+        for dst, src in zip((table, seq, starts), batch_on_device(bt)):
+            dst.copy_(src)
+        for dst, src in zip(state, to_dev(cache)):
+            dst.copy_(src)
+        for dst, src in zip((q, k, v), z):
+            dst.copy_(src[0])
+        graphs[turn % 2].replay()
+        graphs[(turn + 1) % 2].replay()  # again with the same tokens: nothing changes
+        torch.cuda.synchronize()
+        ref = [np.array(c) for c in cache]
+        want = kv_ref.append(ref, bt["table"], bt["lens"], bt["q_start"], z[1][1], z[2][1], z[0][1], rope_np)
+        assert all(same_bits(s.cpu().numpy(), c) for s, c in zip(state, ref))
+        exact = kv_ref.attention(ref, bt["table"], bt["lens"], bt["q_start"], want)
+        bound = kv_ref.attention_bound(ref, bt["table"], bt["lens"], bt["q_start"], want, exact)
+        o = [out.float().cpu().numpy() for out in outs]
+        assert same_bits(o[0], o[1])
+        assert (np.abs(o[0] - exact) <= bound).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_two_calls_at_once(n):
+    """Two streams, two batches over one cache, each call with its own workspace (made by the call)."""
+    hq, hk, d, page = 8, 2, 128, 32
+    bs = [make_batch([n] * 6, [300 + 40 * i for i in range(6)], page, 631 + s) for s in range(2)]
+    pages = max(b["pages"] for b in bs)
+    cache = make_cache(pages, hk, page, d, 633)
+    dc = to_dev(cache)
+    qs = [rows((b["rows"], hq, d), 635 + i) for i, b in enumerate(bs)]
+    meta = [batch_on_device(b) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            outs[i].append(tw.bitnet_attention(dc, *meta[i], qs[i][0], n, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, b in enumerate(bs):
+        exact = kv_ref.attention(cache, b["table"], b["lens"], b["q_start"], qs[i][1])
+        bound = kv_ref.attention_bound(cache, b["table"], b["lens"], b["q_start"], qs[i][1], exact)
+        for o in outs[i]:
+            assert (np.abs(o.float().cpu().numpy() - exact) <= bound).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_output_over_the_queries(n):
+    b = make_batch([n, n], [90, n], 32, 641)
+    cache = make_cache(b["pages"], 2, 32, 128, 642, b["free"])
+    q, _ = rows((b["rows"], 4, 128), 643)
+    args = (to_dev(cache), *batch_on_device(b))
+    want = tw.bitnet_attention(*args, q, n)
+    got = tw.bitnet_attention(*args, q, n, out=q)
+    torch.cuda.synchronize()
+    assert got is q and torch.equal(q, want)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_padding_and_free_memory_have_no_effect(n):
+    """Infinities and NaN in rows of no sequence, in steps of free pages, in table entries behind a
+    sequence's last page; any bytes in slots behind its last token."""
+    b = make_batch([n, n], [n + 3, 77], 16, 651, behind=4, width=9)
+    cache = make_cache(b["pages"], 2, 16, 64, 652, b["free"])
+    q, _ = rows((b["rows"], 4, 64), 653)
+    out = [marked(q.shape), marked(q.shape)]
+    tw.bitnet_attention(to_dev(cache), *batch_on_device(b), q, n, out=out[0])
+    q[2 * n:] = float("nan")
+    cache[2][b["free"]] = np.inf
+    cache[3][b["free"]] = -np.inf
+    for s in range(2):
+        last = int(b["lens"][s]) - 1
+        for c in cache[:2]:
+            c[b["table"][s, last // 16], :, last % 16 + 1:] = -128
+    b["table"][b["table"] < 0] = 2 ** 31 - 1
+    tw.bitnet_attention(to_dev(cache), *batch_on_device(b), q, n, out=out[1])
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[1]) and (out[0][2 * n:] == MARK).all()
+
+
+BAD = [("page", lambda b: b["table"].__setitem__(1, 10 ** 6)),
+       ("negative page", lambda b: b["table"].__setitem__(1, -1)),
+       ("length beyond the table", lambda b: b["lens"].__setitem__(1, 10 ** 6)),
+       ("negative length", lambda b: b["lens"].__setitem__(1, -5)),
+       ("rows beyond T", lambda b: b["q_start"].__setitem__(3, 10 ** 6)),
+       ("decreasing rows", lambda b: b["q_start"].__setitem__(2, 0))]
+
+
+@pytest.mark.parametrize("what,spoil", BAD, ids=[w for w, _ in BAD])
+@pytest.mark.parametrize("n", [2, 40])
+def test_bad_batches_are_refused_on_the_device(what, spoil, n):
+    """Contradictory batches set the status word and touch nothing outside the sequences concerned (shown on
+    the CPU: every access of the kernels lies behind the checks of seq_info / attn_seq / page_of)."""
+    b = make_batch([n, n, n], [n + 20, n + 30, n + 9], 16, 661)
+    cache = make_cache(b["pages"], 2, 16, 64, 662)
+    q, _ = rows((b["rows"], 4, 64), 663)
+    k, _ = rows((b["rows"], 2, 64), 664)
+    good = to_dev(cache)
+    first = tw.bitnet_attention(good, *batch_on_device(b), q, n)
+    tw.bitnet_kv_append(good, *batch_on_device(b), k, k)
+    assert tw.bitnet_batch_status() == 0
+    spoil(b)
+    args = batch_on_device(b)
+    dc = to_dev(cache)
+    got = tw.bitnet_attention(dc, *args, q, n)
+    assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
+    assert tw.bitnet_batch_status() == 0
+    tw.bitnet_kv_append(dc, *args, k, k)
+    assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
+    if what == "decreasing rows":
+        return  # the last sequence then claims the first one's rows too
+    assert torch.equal(got[:n], first[:n])  # the sound first sequence
+    page = int(b["table"][0, (n + 20 - 1) // 16])
+    assert torch.equal(dc.k[page], good.k[page]) and torch.equal(dc.v_step[page], good.v_step[page])
+
+
+def test_more_new_tokens_than_said_and_short_rotation_tables():
+    b = make_batch([3, 1], [30, 20], 16, 671)
+    cache = make_cache(b["pages"], 2, 16, 64, 672)
+    q, qf = rows((4, 4, 64), 673)
+    out = tw.bitnet_attention(to_dev(cache), *batch_on_device(b), q, 2)
+    assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
+    exact = kv_ref.attention(cache, b["table"], b["lens"], b["q_start"], qf)
+    assert np.allclose(out[3].float().cpu().numpy(), exact[3], rtol=0.02, atol=0.02)
+    k, _ = rows((4, 2, 64), 674)
+    dc = to_dev(cache)
+    tw.bitnet_kv_append(dc, *batch_on_device(b), k, k, rope=dev(kv_ref.rope_table(25, 64)))
+    assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
+    assert same_bits(dc.k[int(b["table"][0, 1])].cpu().numpy(), cache[0][int(b["table"][0, 1])])
+
+
+def test_append_with_fewer_cached_than_new_tokens_is_refused():
+    b = make_batch([5], [5], 16, 681)
+    cache = make_cache(b["pages"], 1, 16, 64, 682)
+    b["lens"][0] = 3
+    k, _ = rows((5, 1, 64), 683)
+    dc = to_dev(cache)
+    tw.bitnet_kv_append(dc, *batch_on_device(b), k, k)
+    assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
+    assert all(same_bits(x.cpu().numpy(), y) for x, y in zip(dc, cache))
+
+
+def test_a_bad_batch_leaves_later_calls_alone():
+    """The batch status is a word of its own: the BitLinear calls' waits do not give up over it."""
+    from gpu_util import make_weights, make_x
+    b = make_batch([1], [20], 16, 691)
+    cache = make_cache(b["pages"], 1, 16, 64, 692)
+    b["table"][:] = 10 ** 6
+    q, _ = rows((1, 1, 64), 693)
+    tw.bitnet_attention(to_dev(cache), *batch_on_device(b), q, 1)
+    W = make_weights(512, 256, 694)
+    x, _ = make_x(300, 256, 695)
+    y = tw.bitnet_linear(x, W["p"], W["g"])
+    assert tw.bitnet_device_status() == 0
+    assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
+    assert torch.equal(y, tw.bitnet_linear(x, W["p"], W["g"]))
