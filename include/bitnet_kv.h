@@ -136,7 +136,7 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
  *              (multiple of 8, at least n_heads * head_dim)
  *   n_heads    multiple of the cache's n_kv_heads, at most 128 per kv head
  *   max_new    at least the largest n_b, 1 .. T; it chooses the kernel: up to
- *              32 rows (max_new times query heads per kv head) the one for few
+ *              48 rows (max_new times query heads per kv head) the one for few
  *              new tokens, above that the one for prompts.  Either takes any
  *              n_b <= max_new, 0 included.
  *   scale      finite, > 0; 1 / sqrt(head_dim) in BitNet

@@ -1,5 +1,5 @@
 // attention_tokens.cuh -- attention of few new tokens per sequence over the
-// paged 8-bit cache (decoding, verification of drafts): at most 32 query rows
+// paged 8-bit cache (decoding, verification of drafts): at most 48 query rows
 // (new tokens x query heads of the group) per sequence and kv head.
 //
 //   o_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp2(c (q_r . k_j) - m_r),
@@ -41,7 +41,12 @@
 namespace bitnet {
 
 constexpr int AT_GROUP = 16;    // tokens a warp takes at a time (a page holds at least as many): a unit
-constexpr int AT_MAX_ROWS = 32; // query rows per (sequence, kv head)
+// Query rows per (sequence, kv head) that this kernel is chosen for.  Its cost grows with every
+// 16 rows, that of the kernel for prompts with every 256; measured with 48 and 64 rows: 64
+// sequences of 2048 tokens 117 and 150 us here, 141 and 141 us there; with 64 rows 16 sequences
+// of 8192 tokens (8 query heads a kv head) 117 us here, 107 us there, 64 sequences of 300 tokens
+// 46 and 55 us.
+constexpr int AT_MAX_ROWS = 48;
 constexpr int AT_MAX_CTAS = 160;
 constexpr int AT_MIN_UNITS = 16; // groups worth a CTA of their own
 constexpr float AT_LAZY = 8.0f;  // a row's exponents refer to a maximum up to 2^8 behind
@@ -70,6 +75,8 @@ struct AttnArgs {
 };
 
 // Warps for nq tiles of 8 rows: as many as leave each the registers it wants (168, 255).
+// Tiles of 8 rows serve up to 8 rows (16 sequences of 8192 tokens, 8 rows: 40.5 us, against 47.1
+// in a tile of 16), tiles of 16 more (16 rows: 49 us).
 // With 16 and 12 warps of 128 and 168: 52 us instead of 47 (64 sequences), 64 instead of 48
 // (16 sequences of four new tokens, 8 query heads a kv head).
 constexpr __host__ __device__ int at_warps(int nq) { return nq == 1 ? 12 : 8; }

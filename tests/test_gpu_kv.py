@@ -184,7 +184,7 @@ def test_tokens_lengths(page, d):
 
 
 @pytest.mark.parametrize("hq,hk,n", [(20, 5, 1), (1, 1, 1), (16, 1, 1), (5, 1, 3), (32, 1, 1), (7, 1, 4), (12, 4, 8),
-                                     (6, 6, 16), (3, 3, 32)])
+                                     (6, 6, 16), (3, 3, 32), (12, 1, 4), (2, 2, 47)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_tokens_heads_and_drafts(hq, hk, n, d):
     """Groups of any size, several new tokens (each sees itself and what came before), some sequences
