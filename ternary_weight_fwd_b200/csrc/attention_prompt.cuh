@@ -9,11 +9,15 @@
 // of the group (row = token * group + head).  An MMA tile holds as many whole
 // tokens as fit its 128 rows, a row tile is two of them, A and B, so that one's
 // softmax runs while the other's products do.  Tokens are taken in blocks of 128.
-// The work is the list of all (sequence, kv head, row tile, block that the tile
-// sees), with two more units per tile for loading its queries and storing its
-// rows, cut into equal contiguous shares, one per CTA (one CTA per SM); tiles
-// that two or more CTAs share are joined by k_attention_prompt_join through the
-// workspace, in the order of the CTAs.
+// One CTA per SM.  Where no tile is dearer than a CTA's even share of the work, the
+// CTAs claim whole tiles, dearest first (k_attention_plan sorts them), each when its
+// last copies of the tile before are under way.  Else (few rows, long contexts) the
+// list of all (sequence, kv head, row tile, block that the tile sees), with two more
+// units per tile for loading its queries and storing its rows, is cut into equal
+// contiguous shares, and tiles that two or more CTAs share are joined by
+// k_attention_prompt_join through the workspace, in the order of the CTAs.  (Equal
+// shares always: 144 us for a 4096-token prompt, the parts of 147 shared tiles
+// written and read again.)  Which CTA takes a tile does not change its result.
 //
 // One CTA, 24 warps:
 //   warps 0-7, 8-15 softmax of tile A, B: two threads per row, 64 tokens of a block
@@ -84,27 +88,57 @@ BITNET_DEVINL int64_t ap_active(int64_t units, int ctas)
     return want < ctas ? want : ctas;
 }
 
-// First unit of every sequence: a warp per sequence adds up its tiles' blocks, then one scan.
-__global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a)
+// Calls f(b, sequence, tile, blocks) for every row tile of one kv head, spread over the
+// CTA's threads: a thread per sequence where there are many, else a warp.
+template <typename F>
+BITNET_DEVINL void ap_for_tiles(const AttnArgs &a, F f)
+{
+    const bool many = a.bt.n_seqs >= 256;
+    const int first = many ? threadIdx.x : threadIdx.x >> 5, step = many ? 1024 : 32;
+    for (int b = first; b < a.bt.n_seqs; b += step) {
+        const AttnSeq s = attn_seq(a, b);
+        const int nt = ap_tiles(s, a.group);
+        for (int t = many ? 0 : threadIdx.x & 31; t < nt; t += many ? 1 : 32) f(b, s, t, ap_blocks(s, a.group, t));
+    }
+}
+
+// One CTA: first unit of every sequence, the choice between whole tiles and shares, the
+// tiles in order of their cost, rows that see nothing.
+template <int D>
+__global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a, int ctas)
 {
     __shared__ int64_t s_sum[32];
     __shared__ int64_t s_carry;
+    __shared__ int s_most, s_tiles, s_bin[1024], s_wsum[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     pdl_wait();
-    const int n_seqs = a.bt.n_seqs;
-    for (int b = warp; b < n_seqs; b += 32) {
-        const AttnSeq s = attn_seq(a, b);
-        const int nt = ap_tiles(s, a.group);
-        int64_t sum = 0;
-        for (int t = lane; t < nt; t += 32) sum += ap_units(ap_blocks(s, a.group, t));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) a.base[b + 1] = sum * a.kv.hk;
-    }
+    const int n_seqs = a.bt.n_seqs, hk = a.kv.hk;
     if (tid == 0) {
         a.base[0] = 0;
         s_carry = 0;
+        s_most = 0;
+        s_tiles = 0;
+    }
+    s_bin[tid] = 0;
+    for (int k = tid; k < ctas; k += 1024) a.shared[k].nrow = 0;
+    for (int b = tid; b < n_seqs; b += 1024) a.base[b + 1] = 0;
+    __syncthreads();
+    int most = 0, tiles = 0;
+    ap_for_tiles(a, [&](int b, const AttnSeq &s, int t, int blocks) {
+        atomicAdd(reinterpret_cast<unsigned long long *>(&a.base[b + 1]), (unsigned long long)ap_units(blocks) * hk);
+        most = max(most, blocks);
+        tiles += blocks > 0;
+        if (blocks == 0) // rows in front of their sequence's first token
+            for (int i = 2 * t * ap_tokens(a.group); i < min(s.n, 2 * (t + 1) * ap_tokens(a.group)); ++i)
+                for (int x = 0; x < hk * a.group * (D / 8); ++x)
+                    reinterpret_cast<uint4 *>(a.out + (int64_t)(s.q0 + i) * a.out_stride)[x] = make_uint4(0, 0, 0, 0);
+    });
+    most = __reduce_max_sync(0xffffffffu, most);
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (lane == 0) {
+        atomicMax(&s_most, most);
+        atomicAdd(&s_tiles, tiles);
     }
     __syncthreads();
     for (int b0 = 0; b0 < n_seqs; b0 += 1024) {
@@ -124,6 +158,43 @@ __global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a)
         if (tid == 1023) s_carry = before + v;
         __syncthreads();
     }
+    const int64_t total = s_carry;
+    most = s_most;
+    // sequences that claim the same rows (a batch that is refused) may have more tiles than fit
+    const bool fits = (int64_t)s_tiles <= a.bt.T / (2 * ap_tokens(a.group)) + n_seqs;
+    const bool whole = fits && (int64_t)ap_units(most) * ctas <= total;
+    if (!fits && tid == 0) record_batch_error();
+    if (tid == 0) {
+        a.claim->whole = whole;
+        a.claim->next = 0;
+        a.claim->tiles = s_tiles * hk;
+    }
+    if (!whole) return;
+    // sorted by cost into 1024 bins, dearest first; the order within one is of no account
+    const float scale = 1023.0f / (float)most;
+    auto bin = [&](int blocks) { return 1023 - min(1023, (int)((float)blocks * scale)); };
+    ap_for_tiles(a, [&](int b, const AttnSeq &s, int t, int blocks) {
+        if (blocks > 0) atomicAdd(&s_bin[bin(blocks)], hk);
+    });
+    __syncthreads();
+    int v = s_bin[tid];
+    const int mine = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += up;
+    }
+    if (lane == 31) s_wsum[warp] = v;
+    __syncthreads();
+    int before = v - mine;
+    for (int w = 0; w < warp; ++w) before += s_wsum[w];
+    s_bin[tid] = before;
+    __syncthreads();
+    ap_for_tiles(a, [&](int b, const AttnSeq &s, int t, int blocks) {
+        if (blocks == 0) return;
+        const int at = atomicAdd(&s_bin[bin(blocks)], hk);
+        for (int h = 0; h < hk; ++h) a.tiles[at + h] = {b, t * hk + h};
+    });
 }
 
 // Walks the unit list tile by tile.  A whole warp runs it.
@@ -295,7 +366,8 @@ struct ApSeg {
     int j0, nkv;     // the first of them; blocks that the tile sees
     int b, h, qt;
     int q0, n, len;  // AttnSeq of b
-    int pad[3];
+    int last;        // the CTA that holds the tile's last block
+    int pad[2];
 };
 
 template <int N>
@@ -383,7 +455,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     constexpr uint32_t R_TILE = AP_BLOCK * D;       // int8 tile
     constexpr uint32_t SLAB = 128 * 128;            // 64 elements of 128 rows
     constexpr int GROUPS = AP_BLOCK / AT_GROUP;
-    static_assert(384 + AP_STEPS * sizeof(ApSteps) <= 1024 && 1024 + AP_SEGS * sizeof(ApSeg) + 4096 <= AP_HDR, "header");
+    static_assert(sizeof(ApSteps) == 160 && 384 + AP_STEPS * sizeof(ApSteps) <= 1024 && 1024 + AP_SEGS * sizeof(ApSeg) + 4096 <= AP_HDR, "header");
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
@@ -400,7 +472,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     uint64_t *p_full = s_full + 2;         // [2][2] weights of the block's halves are
     uint64_t *o_full = p_full + 4;         // [2] a tile's sums are complete
     uint64_t *pair = o_full + 2;           // [8] the two warps of 32 rows exchange a value per row
-    uint64_t *mma_done = pair + 8;
+    uint64_t *seg_want = pair + 8;         // the producer asks for the next tile
+    uint64_t *mma_done = seg_want + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     ApSteps *s_step = reinterpret_cast<ApSteps *>(smem + 384);              // [AP_STEPS]
     ApSeg *s_seg = reinterpret_cast<ApSeg *>(smem + 1024);                  // [AP_SEGS]
@@ -432,6 +505,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             mbar_init(&o_full[x], 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(&pair[i], 2);
+        mbar_init(seg_want, 1);
         mbar_init(mma_done, 1);
         fence_mbarrier_init();
     }
@@ -479,20 +553,45 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         // ---------------- tiles ----------------
         const int64_t total = a.base[a.bt.n_seqs];
         const int64_t active = ap_active(total, gridDim.x);
-        const bool idle = blockIdx.x >= active;
+        const bool whole = a.claim->whole != 0, idle = whole || blockIdx.x >= active;
         const int64_t u0 = idle ? 0 : total * blockIdx.x / active, u1 = idle ? 0 : total * (blockIdx.x + 1) / active;
         ApIter it;
         it.first = 0;
+        it.b = it.h = it.qt = it.nkv = 0;
+        it.s = {0, 0, 0};
         if (u0 < u1) it.seek(a, u0);
+        uint32_t rph = 0;
+        bool first = true;
         for (bool more = true; more;) {
-            int j0 = 0, j1 = 0; // this share's blocks of the tile
-            more = false;
-            while (it.first < u1 && !more) {
-                j0 = (int)max((int64_t)0, u0 - it.first - AP_OVER);
-                j1 = (int)min((int64_t)it.nkv, u1 - it.first - AP_OVER);
-                more = j1 > j0;
-                if (!more) it.next(a);
-                if (it.b >= a.bt.n_seqs) break;
+            int j0 = 0, j1 = 0; // this CTA's blocks of the tile
+            if (whole) {
+                // claimed when the producer asks for the next tile, not before: tiles go to whoever is free
+                if (!first) {
+                    if (!wait(seg_want, rph)) break;
+                    rph ^= 1;
+                }
+                first = false;
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&a.claim->next, 1);
+                at = __shfl_sync(0xffffffffu, at, 0);
+                more = at < a.claim->tiles;
+                if (more) {
+                    const int2 tile = a.tiles[at];
+                    it.b = tile.x;
+                    it.qt = tile.y / a.kv.hk;
+                    it.h = tile.y - it.qt * a.kv.hk;
+                    it.s = attn_seq(a, it.b);
+                    it.nkv = j1 = ap_blocks(it.s, a.group, it.qt);
+                }
+            } else {
+                more = false;
+                while (it.first < u1 && !more) {
+                    j0 = (int)max((int64_t)0, u0 - it.first - AP_OVER);
+                    j1 = (int)min((int64_t)it.nkv, u1 - it.first - AP_OVER);
+                    more = j1 > j0;
+                    if (!more) it.next(a);
+                    if (it.b >= a.bt.n_seqs) break;
+                }
             }
             if (!wait(&seg_empty[gslot], gph ^ 1)) break;
             if (lane == 0) {
@@ -506,6 +605,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 d.q0 = it.s.q0;
                 d.n = it.s.n;
                 d.len = it.s.len;
+                d.last = !whole && more ? (int)(((it.first + AP_OVER + it.nkv) * active - 1) / total) : 0;
                 mbar_arrive(&seg_full[gslot]);
                 if (more) { // the queries are on their way to the L2 cache by the time they are asked for
                     const int tokens = ap_tokens(a.group);
@@ -519,8 +619,10 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 gslot = 0;
                 gph ^= 1;
             }
-            if (more) it.next(a);
-            if (it.b >= a.bt.n_seqs) it.first = u1;
+            if (!whole) {
+                if (more) it.next(a);
+                if (it.b >= a.bt.n_seqs) it.first = u1;
+            }
         }
       } else if (warp == AP_TMA_WARP) {
         // ---------------- producer ----------------
@@ -546,6 +648,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             }
             if (++j >= sg.cnt) {
                 j = 0;
+                if (lane == 0) mbar_arrive(seg_want);
                 more = next_seg();
             }
         };
@@ -935,6 +1038,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             const float us = unit == AP_NO_UNIT ? 0.0f : exp2_int(unit);
             const float inv = m > -INFINITY ? us / l : 0.0f;
             const int64_t part = (2 * (int64_t)blockIdx.x + (sg.j0 == 0 ? 1 : 0)) * AP_ROWS;
+            if (!whole && sg.j0 == 0 && warp == 0 && lane == 0)
+                a.shared[blockIdx.x] = {sg.n, sg.last, sg.q0, sg.h, sg.qt};
             if (!whole && live && half == 0) a.part_ml[part + x * 128 + r] = make_float2(m, l);
             const int64_t row_at = live ? (int64_t)(sg.q0 + tok) * a.out_stride +
                                               ((int64_t)sg.h * a.group + rhead) * D + half * (D / 2)
@@ -984,67 +1089,32 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     }
 }
 
-// Joins the row tiles that more than one CTA shared and writes zeros for tiles
-// that see nothing.  Tiles are numbered per kv head so that sequence b's start
-// at q_start[b] / tokens + b (there is room for each one's tiles).  A thread per
-// row and 16 columns.
+// Joins the row tiles that more than one CTA shared: blocks (k, .) the one whose first
+// part CTA k holds, a thread per row and 16 columns.
 template <int D>
-__global__ void __launch_bounds__(256) k_attention_prompt_join(const AttnArgs a, int ctas)
+__global__ void __launch_bounds__(256) k_attention_prompt_join(const AttnArgs a)
 {
-    __shared__ int s_seq;
-    __shared__ int64_t s_before[8];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) s_seq = -1;
     pdl_launch_dependents();
     pdl_wait();
-    __syncthreads();
-    const int64_t item = blockIdx.x;
-    const int tokens = ap_tokens(a.group), tile = 2 * tokens;
-    for (int b = tid; b < a.bt.n_seqs; b += 256) {
-        const int64_t lo = a.bt.q_start[b], hi = a.bt.q_start[b + 1];
-        if (lo >= 0 && hi >= lo && hi <= a.bt.T && item >= lo / tile + b && item < hi / tile + b + 1) s_seq = b;
-    }
-    __syncthreads();
-    const int b = s_seq, h = blockIdx.y;
-    if (b < 0) return;
-    const AttnSeq s = attn_seq(a, b);
-    const int64_t qt64 = item - (s.q0 / tile + b);
-    if (s.n == 0 || qt64 >= ap_tiles(s, a.group)) return;
-    const int qt = (int)qt64;
-    const int nkv = ap_blocks(s, a.group, qt);
-    int64_t before = 0;
-    for (int t = tid; t < qt; t += 256) before += ap_units(ap_blocks(s, a.group, t));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    if (lane == 0) s_before[warp] = before;
-    __syncthreads();
-    before = 0;
-    for (int w = 0; w < 8; ++w) before += s_before[w];
-    const int64_t total = a.base[a.bt.n_seqs], first = a.base[b];
-    const int64_t ub = first + (a.base[b + 1] - first) / a.kv.hk * h + before;
-    int c0 = 0, c1 = -1;
-    if (nkv > 0) {
-        const int64_t active = ap_active(total, ctas);
-        c0 = (int)(((ub + AP_OVER + 1) * active - 1) / total); // holds the first block
-        c1 = (int)(((ub + AP_OVER + nkv) * active - 1) / total);
-        if (c0 == c1) return;
-    }
+    const int tid = threadIdx.x, c0 = blockIdx.x;
+    const AttnShared s = a.shared[c0]; // nrow: the sequence's new tokens, r0: the tile
+    if (s.nrow == 0) return;
+    const int tokens = ap_tokens(a.group);
     const int rtok = (tid & 127) / a.group, g = (tid & 127) - rtok * a.group;
-    const int tok = (2 * qt + (tid >> 7)) * tokens + rtok;
-    if (rtok >= tokens || tok >= s.n) return;
+    const int tok = (2 * s.r0 + (tid >> 7)) * tokens + rtok;
+    if (rtok >= tokens || tok >= s.nrow) return;
+    auto part = [&](int k) { return (2 * (int64_t)k + (k == c0 ? 1 : 0)) * AP_ROWS; };
     float m = -INFINITY, l = 0.0f;
-    for (int k = c0; k <= c1; ++k)
-        m = fmaxf(m, a.part_ml[(2 * (int64_t)k + (k == c0 ? 1 : 0)) * AP_ROWS + tid].x);
+    for (int k = c0; k <= s.last; ++k) m = fmaxf(m, a.part_ml[part(k) + tid].x);
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    const int col = blockIdx.z * 16;
-    for (int k = c0; k <= c1; ++k) {
-        const int64_t part = (2 * (int64_t)k + (k == c0 ? 1 : 0)) * AP_ROWS;
-        const float2 ml = a.part_ml[part + tid];
+    const int col = blockIdx.y * 16;
+    for (int k = c0; k <= s.last; ++k) {
+        const float2 ml = a.part_ml[part(k) + tid];
         const float f = ml.x == -INFINITY ? 0.0f : fast_exp2(ml.x - m);
         l += ml.y * f;
-        const float4 *src = reinterpret_cast<const float4 *>(a.part + part * D) + (col / 4) * AP_ROWS + tid;
+        const float4 *src = reinterpret_cast<const float4 *>(a.part + part(k) * D) + (col / 4) * AP_ROWS + tid;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float4 v = src[i * AP_ROWS];
@@ -1056,7 +1126,7 @@ __global__ void __launch_bounds__(256) k_attention_prompt_join(const AttnArgs a,
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)(s.q0 + tok) * a.out_stride +
-                                           ((int64_t)h * a.group + g) * D + col);
+                                           ((int64_t)s.h * a.group + g) * D + col);
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)

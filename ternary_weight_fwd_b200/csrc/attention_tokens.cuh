@@ -58,6 +58,11 @@ struct AttnShared {
     int q0, h, r0;
 };
 
+// Prompts: whether whole tiles are claimed, the next one and how many there are.
+struct AttnClaim {
+    int whole, next, tiles;
+};
+
 struct AttnArgs {
     KvView kv;
     BatchView bt;
@@ -71,7 +76,9 @@ struct AttnArgs {
     float *part;       // [2 * CTAs][rows][D] partial sums
     float2 *part_ml;   // [2 * CTAs][rows] their maxima and sums
     int64_t *base;     // [n_seqs + 1] first unit of each sequence (prompts)
-    AttnShared *shared; // [CTAs] row tiles to join (few tokens)
+    AttnShared *shared; // [CTAs] row tiles to join
+    AttnClaim *claim;   // (prompts)
+    int2 *tiles;        // (prompts) sequence, tile * kv heads + head, dearest first
 };
 
 // Warps for nq tiles of 8 rows: as many as leave each the registers it wants (168, 255).

@@ -115,8 +115,9 @@ bool encode_queries(CUtensorMap *map, const void *q, int64_t T, int64_t stride, 
 struct AttnPlan {
     bool ok;
     int nq; // tiles of 8 rows of the kernel for few tokens (1 or 2); 0: the kernel for prompts
-    size_t base_bytes, ml_bytes, part_bytes; // units' bases or shared row tiles; parts' maxima and sums; parts
-    size_t total() const { return base_bytes + ml_bytes + part_bytes; }
+    size_t shared_bytes, ml_bytes, part_bytes; // claim and shared row tiles; parts' maxima and sums; parts
+    size_t base_bytes, tile_bytes;             // prompts: units' bases, tiles by cost
+    size_t total() const { return shared_bytes + ml_bytes + part_bytes + base_bytes + tile_bytes; }
 };
 
 AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d, int64_t max_new)
@@ -128,7 +129,14 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t T, int64_t n_heads, int64_t hk, int d
     const int64_t rows = n_heads / hk * max_new;
     p.nq = rows <= 8 ? 1 : rows <= AT_MAX_ROWS ? 2 : 0;
     const size_t part_rows = (size_t)2 * AT_MAX_CTAS * (p.nq ? 8 * p.nq : AP_ROWS);
-    p.base_bytes = p.nq ? align_up(AT_MAX_CTAS * sizeof(AttnShared), 256) : align_up((size_t)(n_seqs + 1) * 8, 256);
+    p.shared_bytes = 256 + align_up(AT_MAX_CTAS * sizeof(AttnShared), 256);
+    if (p.nq == 0) {
+        const int64_t tile = 2 * ap_tokens((int)(n_heads / hk));
+        const int64_t tiles = (T / tile + n_seqs) * hk; // at least every sequence's
+        if (tiles > INT32_MAX) return p;
+        p.base_bytes = align_up((size_t)(n_seqs + 1) * 8, 256);
+        p.tile_bytes = (size_t)tiles * sizeof(int2);
+    }
     p.ml_bytes = align_up(part_rows * sizeof(float2), 256);
     p.part_bytes = part_rows * d * sizeof(float);
     p.ok = true;
@@ -158,13 +166,11 @@ cudaError_t launch_prompt(const CUtensorMap &tk, const CUtensorMap &tv, const At
     CUtensorMap tq;
     if (!encode_queries(&tq, a.q, a.bt.T, a.q_stride, a.kv.hk * a.group, a.group, D)) return cudaErrorInvalidValue;
     cudaError_t e = ensure_smem(k_attention_prompt<D>, smem, done, dev);
-    if (e == cudaSuccess) e = launch_pdl(k_attention_plan, dim3(1), dim3(1024), 0, stream, a);
+    if (e == cudaSuccess) e = launch_pdl(k_attention_plan<D>, dim3(1), dim3(1024), 0, stream, a, ctas);
     if (e == cudaSuccess)
         e = launch_pdl(k_attention_prompt<D>, dim3(ctas), dim3(AP_THREADS), smem, stream, tk, tv, tq, a);
     if (e == cudaSuccess)
-        e = launch_pdl(k_attention_prompt_join<D>,
-                       dim3((unsigned)(a.bt.T / (2 * ap_tokens(a.group)) + a.bt.n_seqs), (unsigned)a.kv.hk, D / 16),
-                       dim3(256), 0, stream, a, ctas);
+        e = launch_pdl(k_attention_prompt_join<D>, dim3(ctas, D / 16), dim3(256), 0, stream, a);
     return e;
 }
 
@@ -276,10 +282,15 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
     a.max_new = max_new;
     a.scale_log2 = scale * 1.44269504088896341f;
     char *ws = static_cast<char *>(workspace);
+    a.claim = reinterpret_cast<AttnClaim *>(ws);
+    a.shared = reinterpret_cast<AttnShared *>(ws + 256);
+    ws += p.shared_bytes;
+    a.part_ml = reinterpret_cast<float2 *>(ws);
+    ws += p.ml_bytes;
+    a.part = reinterpret_cast<float *>(ws);
+    ws += p.part_bytes;
     a.base = reinterpret_cast<int64_t *>(ws);
-    a.shared = reinterpret_cast<AttnShared *>(ws);
-    a.part_ml = reinterpret_cast<float2 *>(ws + p.base_bytes);
-    a.part = reinterpret_cast<float *>(ws + p.base_bytes + p.ml_bytes);
+    a.tiles = reinterpret_cast<int2 *>(ws + p.base_bytes);
     const int ctas = std::min(sms, AT_MAX_CTAS);
     const int rows = a.group * max_new;
     cudaError_t e;
