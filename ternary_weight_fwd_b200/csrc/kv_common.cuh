@@ -15,30 +15,27 @@ __device__ int g_batch_status = 0;
 
 BITNET_DEVINL void record_batch_error() { *(volatile int *)&g_batch_status = BITNET_ERR_INVALID_ARG; }
 
-// Out-of-line part of kv_wait: whether to give up (as mbar_wait does), asked every
-// 256 tries.  t0 = 0 at the first question.
-__device__ __noinline__ bool kv_wait_over(unsigned long long *t0)
+// Out-of-line part of kv_wait, asked every 256 tries: 0 to give up (as mbar_wait does),
+// else the time of the first question (t0 = 0: this one).
+__device__ __noinline__ unsigned long long kv_wait_on(unsigned long long t0)
 {
-    if (status_failed()) return true;
-    const uint64_t now = globaltimer_ns();
-    if (*t0 == 0) {
-        *t0 = now;
-        return false;
-    }
-    if (now - *t0 <= wait_limit_ns()) return false;
+    if (status_failed()) return 0;
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) return now;
+    if (now - t0 <= wait_limit_ns()) return t0;
     record_status(BITNET_ERR_TIMEOUT);
-    return true;
+    return 0;
 }
 
-// mbar_wait in few instructions: the kernels below wait at many places, and
-// code beyond the instruction cache costs them more than the waits.
+// mbar_wait in few instructions: the kernel for prompts waits at many places, and
+// code beyond the instruction cache costs it more than the waits.
 BITNET_DEVINL bool kv_wait(uint64_t *bar, uint32_t parity)
 {
     const uint32_t a = smem_u32(bar);
     unsigned long long t0 = 0;
     for (uint32_t spin = 1;; ++spin) {
         if (mbar_try_wait(a, parity)) return true;
-        if ((spin & 255u) == 0 && kv_wait_over(&t0)) return false;
+        if ((spin & 255u) == 0 && (t0 = kv_wait_on(t0)) == 0) return false;
     }
 }
 
