@@ -524,18 +524,22 @@ def _kv_rows(t, name, like, heads, dtype=None):
     return stride[0] if shape[0] > 1 else shape[1] * d
 
 
-def _kv_call(name, index, stream, made, *args):
-    """Call a C entry on device `index` and the given (or that device's current) stream; memory made for
-    the call is kept from reuse until the stream is through with it."""
+def _kv_empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the device's current one).  It comes from that stream's pool:
+    what the current stream's pool hands out may still be in use by work there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _kv_call(name, index, stream, *args):
+    """Call a C entry on device `index` and the given (or that device's current) stream."""
     fn = getattr(load_library(), name)
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)  # torch.cuda.current_stream(index).cuda_stream, 2 us faster
     else:
-        if stream.device.index != index:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{index}")
         raw = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
     if torch.cuda.current_device() == index:
         status = fn(*args, raw)
     else:
@@ -545,17 +549,21 @@ def _kv_call(name, index, stream, made, *args):
         raise BitnetError(status, name)
 
 
+def _kv_stream(stream, index):
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+
+
 def bitnet_rope_table(max_pos, head_dim, theta=ROPE_THETA, *, table=None, device="cuda", stream=None):
     """Rotation table fp32 [max_pos][head_dim]: cosines of a position's angles, then sines."""
-    made = ()
     if table is None:
-        table = torch.empty((max_pos, head_dim), dtype=torch.float32, device=device)
-        made = (table,)
+        table = _kv_empty((max_pos, head_dim), torch.float32, device, stream)
     elif table.dtype != torch.float32 or table.shape != (max_pos, head_dim) or not table.is_contiguous():
         raise ValueError(f"table must be contiguous fp32 [{max_pos}][{head_dim}]")
     if not table.is_cuda:
         raise ValueError(f"table is on {table.device}, not on a GPU")
-    _kv_call("bitnet_rope_table", table.device.index, stream, made, float(theta), max_pos, head_dim, table.data_ptr())
+    _kv_stream(stream, table.device.index)
+    _kv_call("bitnet_rope_table", table.device.index, stream, float(theta), max_pos, head_dim, table.data_ptr())
     return table
 
 
@@ -571,17 +579,16 @@ def bitnet_kv_append(cache, page_table, seq_lens, q_start, k, v, *, q=None, rope
     if v.shape[0] != rows:
         raise ValueError("k and v must have the same rows")
     c, b = _kv_views(cache, page_table, seq_lens, q_start, rows)
+    _kv_stream(stream, kc.get_device())
     qp = op = rp = None
     heads = qs = os_ = rope_len = 0
-    made = ()
     if q is not None:
         qs = _kv_rows(q, "q", kc, None, k.dtype)
         heads = q.shape[1]
         if q.shape[0] != rows:
             raise ValueError("q and k must have the same rows")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-            made = (q_out,)
+            q_out = _kv_empty(q.shape, torch.bfloat16, q.device, stream)
         os_ = _kv_rows(q_out, "q_out", kc, heads, torch.bfloat16)
         if q_out.shape[0] != rows:
             raise ValueError("q_out and q must have the same rows")
@@ -595,7 +602,7 @@ def bitnet_kv_append(cache, page_table, seq_lens, q_start, k, v, *, q=None, rope
                 or rope.get_device() != kc.get_device()):
             raise ValueError(f"rope must be contiguous [positions][{kc.shape[3]}] on {kc.device}")
         rp, rope_len = rope.data_ptr(), rope.shape[0]
-    _kv_call("bitnet_kv_append", kc.get_device(), stream, made, c, b, qp, k.data_ptr(), v.data_ptr(), _dtype_code(k), heads,
+    _kv_call("bitnet_kv_append", kc.get_device(), stream, c, b, qp, k.data_ptr(), v.data_ptr(), _dtype_code(k), heads,
              qs, ks, vs, rp, rope_len, op, os_)
     return q_out
 
@@ -614,20 +621,18 @@ def bitnet_attention(cache, page_table, seq_lens, q_start, q, max_new, *, scale=
     qs = _kv_rows(q, "q", kc, None, torch.bfloat16)
     rows, heads, d = q.shape
     c, b = _kv_views(cache, page_table, seq_lens, q_start, rows)
-    made = ()
+    _kv_stream(stream, kc.get_device())
     if out is None:
-        out = torch.empty((rows, heads, d), dtype=torch.bfloat16, device=q.device)
-        made = (out,)
+        out = _kv_empty((rows, heads, d), torch.bfloat16, q.device, stream)
     os_ = _kv_rows(out, "out", kc, heads, torch.bfloat16)
     if out.shape[0] != rows:
         raise ValueError("out and q must have the same rows")
     if workspace is None:
         need = load_library().bitnet_attention_workspace_size(b.n_seqs, rows, heads, c.n_kv_heads, d, max_new)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        made += (workspace,)
+        workspace = _kv_empty(max(need, 16), torch.uint8, q.device, stream)
     elif workspace.get_device() != q.get_device():
         raise ValueError(f"workspace is on {workspace.device}, the cache on {q.device}")
-    _kv_call("bitnet_attention", kc.get_device(), stream, made, c, b, q.data_ptr(), qs, heads, max_new,
+    _kv_call("bitnet_attention", kc.get_device(), stream, c, b, q.data_ptr(), qs, heads, max_new,
              d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
              workspace.numel() * workspace.element_size())
     return out

@@ -70,6 +70,16 @@ bool rows_share(const void *a, int64_t sa, int64_t wa, const void *b, int64_t sb
     return d < wa || d + wb > sa;
 }
 
+// Whether `bytes` at p share memory with the cache's codes or steps.
+bool hits_cache(const bitnet_kv_cache_t &c, const void *p, int64_t bytes)
+{
+    const ByteRange r = range_of(p, (size_t)bytes);
+    const size_t steps = (size_t)c.num_pages * c.n_kv_heads;
+    const size_t codes = steps * c.page_size * c.head_dim;
+    return overlaps(r, range_of(c.k, codes)) || overlaps(r, range_of(c.v, codes)) ||
+           overlaps(r, range_of(c.k_step, steps * 4)) || overlaps(r, range_of(c.v_step, steps * 4));
+}
+
 template <bool F32, int D>
 cudaError_t launch_append(const AppendArgs &a, int page_shift, dim3 grid, cudaStream_t stream)
 {
@@ -217,7 +227,8 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
         const bool same = q == q_out && size == 2 && q_stride == q_out_stride;
         if ((!same && rows_share(q, q_stride * size, qw * size, q_out, q_out_stride * 2, qw * 2, T)) ||
             rows_share(k, k_stride * size, kw * size, q_out, q_out_stride * 2, qw * 2, T) ||
-            rows_share(v, v_stride * size, kw * size, q_out, q_out_stride * 2, qw * 2, T))
+            rows_share(v, v_stride * size, kw * size, q_out, q_out_stride * 2, qw * 2, T) ||
+            hits_cache(*cache, q_out, ((T - 1) * q_out_stride + qw) * 2))
             return BITNET_ERR_INVALID_ARG;
     }
     a.q = q;
@@ -258,7 +269,7 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
     AttnArgs a = {};
     bitnet_status_t st = check_cache(cache, batch, a.kv, a.bt);
     if (st != BITNET_OK) return st;
-    if (n_heads < 1 || max_new < 1 || max_new > a.bt.T || !(scale > 0.0f) || !std::isfinite(scale))
+    if (n_heads < 1 || max_new < 1 || max_new > a.bt.T || !(scale > 0.0f) || !std::isfinite(scale * 1.4427f))
         return BITNET_ERR_INVALID_ARG;
     const int d = cache->head_dim, hk = cache->n_kv_heads;
     const AttnPlan p = attn_plan(a.bt.n_seqs, a.bt.T, n_heads, hk, d, max_new);
@@ -271,6 +282,12 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
         return BITNET_ERR_INVALID_ARG;
     if (!workspace || ws_bytes < p.total()) return BITNET_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BITNET_ERR_MISALIGNED;
+    const ByteRange wr = range_of(workspace, p.total());
+    const int64_t out_bytes = ((int64_t)(a.bt.T - 1) * out_stride + qw) * 2;
+    if (overlaps(wr, range_of(out, (size_t)out_bytes)) ||
+        overlaps(wr, range_of(q, (size_t)(((int64_t)(a.bt.T - 1) * q_stride + qw) * 2))) ||
+        hits_cache(*cache, out, out_bytes) || hits_cache(*cache, workspace, (int64_t)p.total()))
+        return BITNET_ERR_INVALID_ARG;
     const int dev = current_device();
     const int sms = num_sms_for(dev);
     if (sms <= 0) return BITNET_ERR_CUDA;

@@ -524,3 +524,45 @@ def test_a_bad_batch_leaves_later_calls_alone():
     assert tw.bitnet_device_status() == 0
     assert tw.bitnet_batch_status() == tw.BITNET_ERR_INVALID_ARG
     assert torch.equal(y, tw.bitnet_linear(x, W["p"], W["g"]))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_rows_in_front_of_the_first_sequence(n):
+    """q_start need not begin at 0: rows in front of it are padding like those behind."""
+    b = make_batch([n, n], [n + 30, n], 16, 701)
+    b["q_start"] = b["q_start"] + 5
+    b["rows"] += 5
+    cache = make_cache(b["pages"], 2, 16, 64, 702)
+    (q, qf), (k, kf) = rows((b["rows"], 4, 64), 703), rows((b["rows"], 2, 64), 704)
+    dc, ref = to_dev(cache), [np.array(c) for c in cache]
+    rot = marked(q.shape)
+    tw.bitnet_kv_append(dc, *batch_on_device(b), k, k, q=q, q_out=rot)
+    want = kv_ref.append(ref, b["table"], b["lens"], b["q_start"], kf, kf, qf)
+    out = marked(q.shape)
+    tw.bitnet_attention(dc, *batch_on_device(b), q, n, out=out)
+    torch.cuda.synchronize()
+    assert all(same_bits(x.cpu().numpy(), y) for x, y in zip(dc, ref))
+    assert (rot[:5] == MARK).all() and (out[:5] == MARK).all()
+    assert same_bits(rot[5:].float().cpu().numpy(), want[5:])
+    exact = kv_ref.attention(ref, b["table"], b["lens"], b["q_start"], qf)
+    bound = kv_ref.attention_bound(ref, b["table"], b["lens"], b["q_start"], qf, exact)
+    assert (np.abs(out.float().cpu().numpy() - exact)[5:] <= bound[5:]).all()
+
+
+def test_memory_made_for_another_stream():
+    """What a call makes for itself on a given stream is not memory that the current stream still works on."""
+    b = make_batch([40, 40], [400, 40], 32, 711)
+    cache = make_cache(b["pages"], 2, 32, 128, 712)
+    q, _ = rows((80, 8, 128), 713)
+    args = (to_dev(cache), *batch_on_device(b))
+    want = tw.bitnet_attention(*args, q, 40)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(5):
+        busy = torch.randn(4096, 4096, device=DEV)
+        for _ in range(4):
+            busy = busy @ busy * 1e-2  # frees memory that is still being read on the current stream
+        del busy
+        got = tw.bitnet_attention(*args, q, 40, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

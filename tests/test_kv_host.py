@@ -12,8 +12,11 @@ INVALID, SHAPE, MISALIGNED, WORKSPACE = (tw.BITNET_ERR_INVALID_ARG, tw.BITNET_ER
                                          tw.BITNET_ERR_MISALIGNED, tw.BITNET_ERR_WORKSPACE)
 
 
+C = 1 << 41  # the cache
+
+
 def structs(**kw):
-    a = dict(k=P, v=P, k_step=P, v_step=P, num_pages=8, n_kv_heads=2, page_size=32, head_dim=64, page_table=P,
+    a = dict(k=C, v=C + (1 << 20), k_step=C + (2 << 20), v_step=C + (3 << 20), num_pages=8, n_kv_heads=2, page_size=32, head_dim=64, page_table=P,
              seq_lens=P, q_start=P, table_width=4, n_seqs=3, T=5)
     a.update({x: y for x, y in kw.items() if x in a})
     c = tw.bitnet_kv_cache_t(*(a[x] for x in ("k", "v", "k_step", "v_step", "num_pages", "n_kv_heads", "page_size",
@@ -28,7 +31,7 @@ COMMON = [
     (dict(table_width=0), INVALID), (dict(page_size=48), SHAPE), (dict(page_size=256), SHAPE),
     (dict(head_dim=96), SHAPE), (dict(n_kv_heads=2000), SHAPE), (dict(num_pages=1 << 31), SHAPE),
     (dict(n_seqs=70000), SHAPE), (dict(T=(1 << 24) + 1), SHAPE), (dict(table_width=1 << 27), SHAPE),
-    (dict(k=P + 8), MISALIGNED), (dict(k_step=P + 2), MISALIGNED), (dict(q_start=P + 1), MISALIGNED),
+    (dict(k=C + 8), MISALIGNED), (dict(k_step=C + 2), MISALIGNED), (dict(q_start=P + 1), MISALIGNED),
 ]
 
 
@@ -40,6 +43,7 @@ COMMON = [
     (dict(rope_len=0), INVALID),
     # q_out over the new keys' rows; over q shifted by one row; over q of another type
     (dict(q_out=P + (1 << 20)), INVALID), (dict(q_out=P + 512), INVALID), (dict(q_out=P, dtype=1), INVALID),
+    (dict(q_out=C), INVALID), (dict(q_out=C + (3 << 20)), INVALID),  # over the cache
 ])
 def test_append_refuses(case, expect):
     a = dict(q=P, k_rows=P + (1 << 20), v_rows=P + (2 << 20), dtype=0, heads=4, q_stride=256, k_stride=128, v_stride=128,
@@ -57,12 +61,15 @@ def test_append_refuses(case, expect):
     (dict(max_new=0), INVALID), (dict(max_new=6), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(q_stride=200), SHAPE),
     (dict(out_stride=260), MISALIGNED), (dict(q=P + 8), MISALIGNED), (dict(out=P + 512), INVALID),
-    (dict(ws=None), WORKSPACE), (dict(ws_bytes=100), WORKSPACE), (dict(ws=P + 4), MISALIGNED),
+    (dict(ws=None), WORKSPACE), (dict(ws_bytes=100), WORKSPACE), (dict(ws=P + (4 << 20) + 4), MISALIGNED),
+    (dict(scale=3e38), INVALID), (dict(out=C + 256), INVALID), (dict(ws=C), INVALID), (dict(ws=P), INVALID),
+    (dict(ws=P + (1 << 20)), INVALID),  # over the cache, q, out
 ])
 def test_attention_refuses(case, expect):
     need = tw.bitnet_attention_workspace_size(3, 5, 4, 2, 64, 2)
     assert need > 0
-    a = dict(q=P, q_stride=256, heads=4, max_new=2, scale=0.125, out=P + (1 << 20), out_stride=256, ws=P, ws_bytes=need)
+    a = dict(q=P, q_stride=256, heads=4, max_new=2, scale=0.125, out=P + (1 << 20), out_stride=256, ws=P + (4 << 20),
+             ws_bytes=need)
     a.update(case)
     c, b = structs(**case)
     st = tw.load_library().bitnet_attention(c, b, a["q"], a["q_stride"], a["heads"], a["max_new"], a["scale"], a["out"],
