@@ -3,7 +3,10 @@
 // cores: tcgen05.mma kind::f16 with fp32 accumulators in tensor memory.
 //
 // Same formulas as attention_tokens.cuh.  Bound by the tensor cores and the
-// exponentials: 4 D flops and one exp2 per visible (query head, token) pair.
+// exponentials: 4 D flops and one exp2 per visible (query head, token) pair.  As
+// built, a block of 128 tokens takes 4800 cycles: the softmax of an MMA tile (3000)
+// and its products (1700, queueing included) take turns, since weights lie over their
+// scores, and the two tiles hide each other only in part.
 //
 // Query rows of a (sequence, kv head) are its new tokens times the query heads
 // of the group (row = token * group + head).  An MMA tile holds as many whole
@@ -17,7 +20,8 @@
 // contiguous shares, and tiles that two or more CTAs share are joined by
 // k_attention_prompt_join through the workspace, in the order of the CTAs.  (Equal
 // shares always: 144 us for a 4096-token prompt, the parts of 147 shared tiles
-// written and read again.)  Which CTA takes a tile does not change its result.
+// written and read again; now 131 us, 0.66 PFLOP/s of visible products.)  Which CTA
+// takes a tile does not change its result.
 //
 // One CTA, 24 warps:
 //   warps 0-7, 8-15 softmax of tile A, B: two threads per row, 64 tokens of a block

