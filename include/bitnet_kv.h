@@ -13,7 +13,7 @@
  * with one fp32 step per (page, kv head):
  *
  *   k, v            [num_pages][n_kv_heads][page_size][head_dim] int8
- *   k_step, v_step  [num_pages][n_kv_heads] fp32;  value = code * step
+ *   k_step, v_step  [num_pages][n_kv_heads] fp32, not negative;  value = code * step
  *
  * A batch of sequences is described on the device:
  *

@@ -95,7 +95,7 @@ constexpr __host__ __device__ int at_smem(int d, int nq)
     return 4096 + at_warps(nq) * (AT_BUFS * 2 * AT_GROUP * d + 8 * nq * (d + 4) * 4 + 2 * 8 * nq * 8) + 1024;
 }
 
-// 3-D tiled tensor copy global -> shared (no multicast); c0 is 0 here.
+// 3-D tiled tensor copy global -> shared (no multicast); c0 times the element size a multiple of 16 bytes.
 BITNET_DEVINL void tma_load_3d(uint32_t dst_smem, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
                                uint64_t *bar)
 {
