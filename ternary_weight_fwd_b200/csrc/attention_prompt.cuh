@@ -51,10 +51,10 @@ constexpr int AP_ROWS = 256;      // query rows per tile (two MMA tiles), some o
 constexpr int AP_BLOCK = 128;     // tokens per block
 constexpr int AP_THREADS = 768;
 constexpr int AP_RAW = 3;         // ring of int8 tiles
-constexpr int AP_CONV = 3;        // ring of fp16 tiles
+constexpr int AP_CONV = 3;        // ring of 16-bit tiles
 constexpr int AP_STEPS = 4;       // ring of blocks' steps (see the producer)
-constexpr int AP_OVER = 2;         // units that a tile costs besides its blocks
-constexpr int AP_MIN_UNITS = 4;    // units worth a CTA of their own
+constexpr int AP_OVER = 2;        // units that a tile costs besides its blocks
+constexpr int AP_MIN_UNITS = 4;   // units worth a CTA of their own
 constexpr int AP_SEGS = 4;        // ring of tiles handed out
 constexpr int AP_CONV_WARP0 = 16, AP_TMA_WARP = 20, AP_MMA_WARP = 21, AP_Q_WARP = 22, AP_SCHED_WARP = 23;
 constexpr int AP_SEG_READERS = 23; // warps that read every tile's description
