@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
     uint64_t *q_full = seg_empty + AP_SEGS;
     uint64_t *q_empty = q_full + 1;        // every product of the queries is complete
     uint64_t *s_full = q_empty + 1;        // [2] scores are in tensor memory
-    uint64_t *p_full = s_full + 2;         // [2][2] weights of the block's halves are
+    uint64_t *p_full = s_full + 2;         // [2][2] weights of the block's halves are; the first one's also: all sums
+                                           // are rescaled
     uint64_t *o_full = p_full + 4;         // [2] a tile's sums are complete
     uint64_t *pair = o_full + 2;           // [8] the two warps of 32 rows exchange a value per row
     uint64_t *seg_want = pair + 8;         // the producer asks for the next tile
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         mbar_init(q_empty, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[2 * x], 4);
+            mbar_init(&p_full[2 * x], 8);
             mbar_init(&p_full[2 * x + 1], 4);
             mbar_init(&o_full[x], 1);
         }
@@ -996,6 +997,13 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                         for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al);
                         tmem_st16(to + 16 * c, w);
                     }
+                }
+                // The first half's products add to every column of the sums, and this half holds the upper ones.
+                if (half == 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * x]);
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1

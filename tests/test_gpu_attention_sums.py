@@ -1,0 +1,72 @@
+"""Attention over contexts whose later tokens move the running maxima, sums and units of a row again and again."""
+import numpy as np
+import pytest
+import torch
+
+import kv_exact
+import ternary_weight_fwd_b200 as tw
+from kv_util import DEV, dev, make_batch, make_cache, rows, same_bits, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    tw.bitnet_device_status()
+    tw.bitnet_batch_status()
+    yield
+    assert tw.bitnet_device_status() == 0
+    assert tw.bitnet_batch_status() == 0
+
+
+def check(b, cache, hq, seed, max_new=None, scale=None, qscale=1.5, repeat=1):
+    d = cache[0].shape[3]
+    q, qf = rows((b["rows"], hq, d), seed, scale=qscale)
+    ref, bound = kv_exact.attention(cache, b, qf, scale)
+    args = (to_dev(cache), dev(b["table"]), dev(b["lens"]), dev(b["q_start"]), q,
+            max_new or max(1, int(np.diff(b["q_start"]).max())))
+    first = None
+    for _ in range(repeat):
+        out = tw.bitnet_attention(*args, scale=scale)
+        torch.cuda.synchronize()
+        o = out.float().cpu().numpy()
+        bad = ~(np.abs(o - ref) <= bound)
+        assert not bad.any(), (np.argwhere(bad)[:5], o[bad][:5], ref[bad][:5], bound[bad][:5])
+        assert first is None or same_bits(o, first)
+        first = o
+    return first
+
+
+def along(b, cache, which, f):
+    """Steps `which` (2: keys, 3: values) of the page j of every sequence become f(j)."""
+    for s, length in enumerate(b["lens"].tolist()):
+        for j in range(-(-length // cache[0].shape[2])):
+            cache[which][b["table"][s, j]] = f(j)
+
+
+def grow(b, cache, kind, every):
+    """Pages in runs of `every`.  keys: key steps that grow by 0.05 a run; the largest of 16 or more scores lies about
+    60 * 1.44 * 2 * step in powers of two above 0, so a row's maximum rises by more than 2^8 in most runs.  values:
+    value steps that alternate by 2^7, so the sums change their unit with every run."""
+    if kind == "keys":
+        along(b, cache, 2, lambda j: 0.05 * (1 + j // every))
+    else:
+        along(b, cache, 3, lambda j: 0.02 * (1.0 if j // every % 2 else 2.0 ** -7))
+
+
+WHOLE = ([512, 500, 512, 490, 512, 333], [2048, 1500, 512, 1999, 1024, 2040])
+SHARED = ([150, 77], [4000, 1333])
+
+
+@pytest.mark.parametrize("kind", ["keys", "values"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", [WHOLE, SHARED], ids=["whole", "shared"])
+def test_prompt_sums_that_are_rescaled_in_every_block(lengths, d, kind):
+    """A row's two softmax threads rescale a half of its sums each, and the products of either half of a block's
+    tokens add to all of them: neither may begin before both are done."""
+    hq, hk, page = 20, 5, 64
+    b = make_batch(*lengths, page, 801)
+    assert kv_exact.whole_tiles(b, hq // hk, hk) == (lengths is WHOLE)
+    cache = make_cache(b["pages"], hk, page, d, 802, b["free"])
+    grow(b, cache, kind, 128 // page)
+    check(b, cache, hq, 803, repeat=5)
