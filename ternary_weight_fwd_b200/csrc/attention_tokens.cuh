@@ -537,35 +537,57 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
                     }
                 // a row's reference follows its maximum when it lags too far, and o keeps units near the
                 // current page's v_step: weights times v_step / unit stay in fp16's range, whatever the
-                // steps of other pages
+                // steps of other pages.  A smaller unit makes larger numbers of what o holds already, so it
+                // goes no lower than where those reach 2^120 (later products add less than 2^52); a page
+                // that then lies far below the unit is lost against what the row tile holds.
                 float r = vs * inv_unit;
                 const bool move = vs > 0.0f && !(r >= 0x1p-4f && r <= 0x1p4f);
                 if (__any_sync(0xffffffffu, grown) || move) {
-                    float us = 1.0f;
-                    if (move) {
-                        const float to = unit > 0.0f ? fmaxf(pow2_floor(vs), unit * 0x1p-60f) : pow2_floor(vs);
-                        us = unit > 0.0f ? unit / to : 1.0f;
-                        unit = to;
-                        inv_unit = 1.0f / to;
-                        r = vs * inv_unit;
-                    }
 #pragma unroll
                     for (int t = 0; t < NQ; ++t)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float al = 1.0f;
-                            if (mx[t][e] > m[t][e] + AT_LAZY) {
-                                al = fast_exp2(m[t][e] - mx[t][e]);
-                                m[t][e] = mx[t][e];
-                                l[t][e] *= al;
-                            }
-                            const float ou = al * us;
+                            if (!(mx[t][e] > m[t][e] + AT_LAZY)) continue;
+                            const float al = fast_exp2(m[t][e] - mx[t][e]);
+                            m[t][e] = mx[t][e];
+                            l[t][e] *= al;
 #pragma unroll
                             for (int n = 0; n < DT; ++n) {
-                                o[t][n][e] *= ou;
-                                o[t][n][2 + e] *= ou;
+                                o[t][n][e] *= al;
+                                o[t][n][2 + e] *= al;
                             }
                         }
+                    if (move) {
+                        float om = 0.0f;
+#pragma unroll
+                        for (int t = 0; t < NQ; ++t)
+#pragma unroll
+                            for (int n = 0; n < DT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) om = fmaxf(om, fabsf(o[t][n][e]));
+                        om = warp_max(om);
+                        const float want = pow2_floor(vs);
+                        if (om > 0.0f) {
+                            const float most = fminf(pow2_floor(0x1p120f / om), 0x1p120f);
+                            float us = unit / want;
+                            if (us <= most) {
+                                unit = want;
+                            } else {
+                                us = most;
+                                unit /= us;
+                            }
+#pragma unroll
+                            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+                                for (int n = 0; n < DT; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[t][n][e] *= us;
+                        } else {
+                            unit = want;
+                        }
+                        inv_unit = 1.0f / unit;
+                        r = vs * inv_unit;
+                    }
                 }
                 uint32_t pb[NQ][2];
 #pragma unroll
@@ -621,14 +643,14 @@ __global__ void __launch_bounds__(at_warps(NQ) * 32, 1) k_attention_tokens(const
                 for (int e = 0; e < 2; ++e) {
                     const int r = 8 * t + 2 * c + e;
                     if (r >= nrow) continue;
-                    const float inv = m[t][e] > -INFINITY ? unit / l[t][e] : 0.0f;
+                    const float inv = m[t][e] > -INFINITY ? 1.0f / l[t][e] : 0.0f;
                     const int tok = (r0 + r) / a.group;
                     uint16_t *p = a.out + (int64_t)(it.s.q0 + tok) * a.out_stride +
                                   ((int64_t)h * a.group + (r0 + r - tok * a.group)) * D + (D / 8) * g;
                     uint32_t w[DT];
 #pragma unroll
                     for (int n = 0; n < DT; ++n)
-                        w[n] = bf16_rn_bits(o[t][n][e] * inv) | (bf16_rn_bits(o[t][n][2 + e] * inv) << 16);
+                        w[n] = bf16_rn_bits(o[t][n][e] * inv * unit) | (bf16_rn_bits(o[t][n][2 + e] * inv * unit) << 16);
 #pragma unroll
                     for (int n = 0; n < DT; n += 4)
                         *reinterpret_cast<uint4 *>(p + 2 * n) = make_uint4(w[n], w[n + 1], w[n + 2], w[n + 3]);

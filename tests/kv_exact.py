@@ -40,7 +40,10 @@ def attention(cache, b, q, scale=None):
                 ds *= scale * (d + 8) * 2.0 ** -24
                 seen = (limit + 1).clamp(min=0).double()[:, None]
                 rel = 2 * 2.0 ** -11 + 2 * 2.0 ** -18 + 2 * seen * 2.0 ** -24 + 2 * ds
-                e = (rel * p + p.clamp(max=2.0 ** -21)) @ vd.abs() + o.abs() * 2.0 ** -8
+                # the result's rounding: half a step of bf16, 2^-8 of a normal value; below 2^-126 steps are
+                # 2^(-126 - 7) wide whatever the value, half of one 2^-134
+                half_step = (o.abs() * 2.0 ** -8).clamp(min=2.0 ** -134)
+                e = (rel * p + p.clamp(max=2.0 ** -21)) @ vd.abs() + half_step
             out[q0:q0 + n, h * g:(h + 1) * g] = o.view(n, g, d)
             bound[q0:q0 + n, h * g:(h + 1) * g] = e.view(n, g, d)
     return out.cpu().numpy(), bound.cpu().numpy()

@@ -70,3 +70,40 @@ def test_prompt_sums_that_are_rescaled_in_every_block(lengths, d, kind):
     cache = make_cache(b["pages"], hk, page, d, 802, b["free"])
     grow(b, cache, kind, 128 // page)
     check(b, cache, hq, 803, repeat=5)
+
+
+TINY = [1e-20, 1e-30, 1e-34, 1e-35, 1e-37]
+
+
+@pytest.mark.parametrize("tiny", TINY)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 4])
+def test_tokens_values_of_tiny_steps_behind_ordinary_ones(n, d, tiny):
+    """Ordinary pages, many groups of 16 tokens on pages of tiny values, ordinary ones again: what the sums hold stays
+    finite while their unit follows the pages' steps."""
+    b = make_batch([n] * 3, [300, 64, 2000], 32, 811)
+    cache = make_cache(b["pages"], 2, 32, d, 812, b["free"])
+    along(b, cache, 3, lambda j: tiny if 0 < j % 7 < 6 else 1.0)
+    check(b, cache, 8, 813, max_new=n)
+
+
+@pytest.mark.parametrize("tiny", TINY)
+@pytest.mark.parametrize("n", [1, 4])
+def test_tokens_all_weight_on_tiny_values(n, tiny):
+    """The first page's scores are 0, those behind have maxima of hundreds: what the ordinary page left vanishes and
+    the results are as small as the tiny values, with the same relative precision.  The step of the first page is
+    smaller than e^127 times the tiny one, so its part of the result is below the bound's."""
+    b = make_batch([n] * 2, [400, 90], 16, 821)
+    cache = make_cache(b["pages"], 1, 16, 128, 822, b["free"])
+    along(b, cache, 2, lambda j: 0.0 if j == 0 else 5.0)
+    along(b, cache, 3, lambda j: 1.0 if j == 0 else tiny)
+    check(b, cache, 4, 823, max_new=n)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_tokens_sums_that_are_rescaled_in_every_group(n):
+    for kind in ("keys", "values"):
+        b = make_batch([n] * 4, [1000, 300, 3000, 17], 16, 831)
+        cache = make_cache(b["pages"], 2, 16, 128, 832, b["free"])
+        grow(b, cache, kind, 1)
+        check(b, cache, 8, 833, max_new=n, repeat=3)
