@@ -353,6 +353,9 @@ BITNET_DEVINL int step_exp(float x) { return max((int)((__float_as_uint(x) >> 23
 BITNET_DEVINL float exp2_int(int e) { return __uint_as_float((uint32_t)(max(-126, min(127, e)) + 127) << 23); }
 
 constexpr int AP_NO_UNIT = -1000;
+// The sums' unit stays above 2^-72 of the largest one before it: a token adds less than 2^21 units of its time (weight 2^8,
+// the step's part in it 2, code 2^7, the step's part on it 2^5), 2^31 tokens less than 2^52, and those times 2^72 are finite.
+constexpr int AP_UNIT_DEPTH = 72;
 
 // What the other warps need of a block's pages, made by the producer.
 struct ApSteps {
@@ -671,21 +674,20 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
         fetch(page, row, valid, head, block);
         fetch(page1, row1, valid1, head1, block1);
         steps(page, row, ks, vs);
-        int stage = 0, slot = 0, unit = AP_NO_UNIT;
+        int stage = 0, slot = 0, unit = AP_NO_UNIT, top = AP_NO_UNIT;
         uint32_t phase = 0, issued = 0, last_par = 0;
         while (block && ok) {
             steps(page1, row1, ks1, vs1);
             fetch(page2, row2, valid2, head2, block2);
-            // The sums' unit moves when the largest step of a block leaves [2^-4, 2^5) of it, and
-            // not below 2^-60 of what it was.
-            if (head) unit = AP_NO_UNIT;
+            // The sums' unit moves when the largest step of a block leaves [2^-4, 2^5) of it.  Limiting
+            // each move instead of the whole descent would not do: what a page of step 1 left became
+            // infinite two blocks behind it where steps are 1e-35.
+            if (head) unit = top = AP_NO_UNIT;
             const float vmax = warp_max(vs);
             if (vmax > 0.0f) {
                 const int e = step_exp(vmax);
-                if (unit == AP_NO_UNIT)
-                    unit = e;
-                else if (e - unit < -4 || e - unit > 4)
-                    unit = max(e, unit - 60);
+                if (unit == AP_NO_UNIT || e - unit < -4 || e - unit > 4) unit = max(e, top - AP_UNIT_DEPTH);
+                top = max(top, unit);
             }
             const int ce = max(-24, min(5, step_exp(vs) - unit)); // exponent that goes on the codes
             const float rest = vs > 0.0f ? vs * exp2_int(-(unit + ce)) : 1.0f;
@@ -1048,7 +1050,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
             tc_fence_after();
             const bool whole = sg.cnt == sg.nkv;
             const float us = unit == AP_NO_UNIT ? 0.0f : exp2_int(unit);
-            const float inv = m > -INFINITY ? us / l : 0.0f;
+            const float inv = m > -INFINITY ? 1.0f / l : 0.0f; // us / l may lie below the normal range
             const int64_t part = (2 * (int64_t)blockIdx.x + (sg.j0 == 0 ? 1 : 0)) * AP_ROWS;
             if (!whole && sg.j0 == 0 && warp == 0 && lane == 0)
                 a.shared[blockIdx.x] = {sg.n, sg.last, sg.q0, sg.h, sg.qt};
@@ -1070,8 +1072,8 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[i][e] = bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e]) * inv) |
-                                      (bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e + 1]) * inv) << 16);
+                            o[i][e] = bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e]) * inv * us) |
+                                      (bf16_rn_bits(__uint_as_float(v[8 * i + 2 * e + 1]) * inv * us) << 16);
                     turn4x4(o, lane);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) { // row (lane & ~3) + i, chunk lane & 3

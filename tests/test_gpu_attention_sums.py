@@ -107,3 +107,25 @@ def test_tokens_sums_that_are_rescaled_in_every_group(n):
         cache = make_cache(b["pages"], 2, 16, 128, 832, b["free"])
         grow(b, cache, kind, 1)
         check(b, cache, 8, 833, max_new=n, repeat=3)
+
+
+@pytest.mark.parametrize("tiny", TINY)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", [WHOLE, SHARED], ids=["whole", "shared"])
+def test_prompt_values_of_tiny_steps_behind_ordinary_ones(lengths, d, tiny):
+    """As for few tokens, by blocks of 128 tokens."""
+    hq, hk, page = 20, 5, 128
+    b = make_batch(*lengths, page, 841)
+    assert kv_exact.whole_tiles(b, hq // hk, hk) == (lengths is WHOLE)
+    cache = make_cache(b["pages"], hk, page, d, 842, b["free"])
+    along(b, cache, 3, lambda j: tiny if 0 < j % 7 < 6 else 1.0)
+    check(b, cache, hq, 843)
+
+
+@pytest.mark.parametrize("tiny", [1e-20, 1e-25])
+def test_prompt_all_weight_on_tiny_values(tiny):
+    b = make_batch([150, 60], [900, 290], 128, 851)
+    cache = make_cache(b["pages"], 1, 128, 128, 852, b["free"])
+    along(b, cache, 2, lambda j: 0.0 if j == 0 else 5.0)
+    along(b, cache, 3, lambda j: 1.0 if j == 0 else tiny)
+    check(b, cache, 4, 853)
