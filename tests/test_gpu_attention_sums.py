@@ -89,6 +89,17 @@ def test_tokens_values_of_tiny_steps_behind_ordinary_ones(n, d, tiny):
 
 @pytest.mark.parametrize("tiny", TINY)
 @pytest.mark.parametrize("n", [1, 4])
+def test_tokens_tiny_steps_within_a_warps_share(n, tiny):
+    """As above with so many tokens that a warp adds up groups of ordinary and of tiny pages itself (148 CTAs of 12
+    warps, 16384 groups of one row tile, or 32768 of two)."""
+    b = make_batch([n] * 64, [2048] * 64, 32, 816)
+    cache = make_cache(b["pages"], 2, 32, 128, 817, b["free"])
+    along(b, cache, 3, lambda j: tiny if 0 < j % 5 < 4 else 1.0)
+    check(b, cache, 8, 818, max_new=n)
+
+
+@pytest.mark.parametrize("tiny", TINY)
+@pytest.mark.parametrize("n", [1, 4])
 def test_tokens_all_weight_on_tiny_values(n, tiny):
     """The first page's scores are 0, those behind have maxima of hundreds: what the ordinary page left vanishes and
     the results are as small as the tiny values, with the same relative precision.  The step of the first page is
