@@ -359,7 +359,8 @@ constexpr int AP_UNIT_DEPTH = 72;
 
 // What the other warps need of a block's pages, made by the producer.
 struct ApSteps {
-    float f[8];    // k_step * scale * log2(e), never 0 (scores of masked tokens are -infinity)
+    float f[8];    // k_step * scale * log2(e), never 0: masked scores are -infinity.  2^-149 in place of 0: a sum of
+                   // codes times queries below 2^128 then gives at most 2^-21
     float lg[8];   // log2 of the part of v_step that the weights carry
     float inv[8];  // its inverse
     float mul[8];  // the part that goes on V's codes: a power of two, or 0
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(AP_THREADS, 1)
                 if (!wait(&raw_empty[stage], phase ^ 1)) break;
                 if (kv == 0 && lane < GROUPS) {
                     ApSteps &st = s_step[slot];
-                    st.f[lane] = fmaxf(a.scale_log2 * ks, 1e-37f);
+                    st.f[lane] = fmaxf(a.scale_log2 * ks, 0x1p-149f);
                     st.lg[lane] = log2f(rest);
                     st.inv[lane] = 1.0f / rest;
                     st.mul[lane] = vs > 0.0f ? exp2_int(ce) : 0.0f;

@@ -140,3 +140,12 @@ def test_prompt_all_weight_on_tiny_values(tiny):
     along(b, cache, 2, lambda j: 0.0 if j == 0 else 5.0)
     along(b, cache, 3, lambda j: 1.0 if j == 0 else tiny)
     check(b, cache, 4, 853)
+
+
+@pytest.mark.parametrize("n,length", [(1, 400), (100, 400)])
+def test_pages_of_key_step_zero_have_scores_of_zero(n, length):
+    """However large the queries: with a scale that brings the other pages' scores to the order of 1."""
+    b = make_batch([n], [length], 16, 861)
+    cache = make_cache(b["pages"], 1, 16, 128, 862, b["free"])
+    along(b, cache, 2, lambda j: 0.0 if j % 3 else 0.02)
+    check(b, cache, 2, 863, qscale=1e33, scale=1e-34)
