@@ -126,8 +126,25 @@ __global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a, int c
     }
     s_bin[tid] = 0;
     for (int k = tid; k < ctas; k += 1024) a.shared[k].nrow = 0;
-    for (int b = tid; b < n_seqs; b += 1024) a.base[b + 1] = 0;
+    int64_t claimed = 0; // rows of this thread's sequences
+    for (int b = tid; b < n_seqs; b += 1024) {
+        a.base[b + 1] = 0;
+        claimed += attn_seq(a, b).n;
+    }
+    const int in_warp = __reduce_add_sync(0xffffffffu, (int)min(claimed, int64_t(1) << 25)); // T is at most 2^24
+    if (lane == 0) s_wsum[warp] = in_warp;
     __syncthreads();
+    claimed = 0;
+    for (int w = 0; w < 32; ++w) claimed += s_wsum[w];
+    if (claimed > a.bt.T) {
+        // Sequences that claim the same rows: their tiles may outnumber those that the workspace holds and
+        // 32 bits count, so none is taken.
+        if (tid == 0) {
+            record_batch_error();
+            *a.claim = {1, 0, 0};
+        }
+        return;
+    }
     int most = 0, tiles = 0;
     ap_for_tiles(a, [&](int b, const AttnSeq &s, int t, int blocks) {
         atomicAdd(reinterpret_cast<unsigned long long *>(&a.base[b + 1]), (unsigned long long)ap_units(blocks) * hk);
@@ -164,10 +181,7 @@ __global__ void __launch_bounds__(1024) k_attention_plan(const AttnArgs a, int c
     }
     const int64_t total = s_carry;
     most = s_most;
-    // sequences that claim the same rows (a batch that is refused) may have more tiles than fit
-    const bool fits = (int64_t)s_tiles <= a.bt.T / (2 * ap_tokens(a.group)) + n_seqs;
-    const bool whole = fits && (int64_t)ap_units(most) * ctas <= total;
-    if (!fits && tid == 0) record_batch_error();
+    const bool whole = (int64_t)ap_units(most) * ctas <= total;
     if (tid == 0) {
         a.claim->whole = whole;
         a.claim->next = 0;
