@@ -101,7 +101,11 @@ bitnet_status_t bitnet_rope_table(double theta, int64_t max_pos, int32_t head_di
  *   q_out     [T][n_heads][head_dim] bf16, rows q_out_stride elements apart:
  *             the rotated queries rounded to nearest even.  It may be q itself
  *             (bf16, same stride) and lie between k and v in their rows, but
- *             must not overlap q, k or v otherwise, nor the cache.
+ *             must not overlap q, k or v otherwise, nor the cache, rope or the
+ *             batch.
+ *
+ * The cache's four arrays lie apart from one another and from everything that
+ * the call reads.
  *
  * For each page that gets new tokens, each kv head, and each of K (rotated) and
  * V, with x the new tokens' values there:
@@ -141,11 +145,11 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
  *              n_b <= max_new, 0 included.
  *   scale      finite, > 0; 1 / sqrt(head_dim) in BitNet
  *   out        [T][n_heads][head_dim] bf16, rows out_stride elements apart
- *              (written); must not overlap the cache, nor q, except that it may
- *              be q itself with the same stride
+ *              (written); must not overlap the cache, the batch, nor q, except
+ *              that it may be q itself with the same stride
  *   workspace  device scratch of at least bitnet_attention_workspace_size
- *              bytes, any contents, apart from q, out and the cache; calls that
- *              may overlap on the GPU need separate ones
+ *              bytes, any contents, apart from q, out, the cache and the batch;
+ *              calls that may overlap on the GPU need separate ones
  *
  * Weights and sums of the softmax are fp32; its weights and the queries enter
  * the tensor cores in fp16 (11 bits, queries scaled by a power of two per row),

@@ -70,14 +70,47 @@ bool rows_share(const void *a, int64_t sa, int64_t wa, const void *b, int64_t sb
     return d < wa || d + wb > sa;
 }
 
-// Whether `bytes` at p share memory with the cache's codes or steps.
-bool hits_cache(const bitnet_kv_cache_t &c, const void *p, int64_t bytes)
+// The cache's codes and steps.
+struct CacheRanges {
+    ByteRange r[4];
+    explicit CacheRanges(const bitnet_kv_cache_t &c)
+    {
+        const size_t steps = (size_t)c.num_pages * c.n_kv_heads;
+        const size_t codes = steps * c.page_size * c.head_dim;
+        r[0] = range_of(c.k, codes);
+        r[1] = range_of(c.v, codes);
+        r[2] = range_of(c.k_step, steps * 4);
+        r[3] = range_of(c.v_step, steps * 4);
+    }
+    bool hit(ByteRange x) const
+    {
+        return overlaps(x, r[0]) || overlaps(x, r[1]) || overlaps(x, r[2]) || overlaps(x, r[3]);
+    }
+    bool apart() const // from one another
+    {
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < i; ++j)
+                if (overlaps(r[i], r[j])) return false;
+        return true;
+    }
+};
+
+// Page table, lengths and row starts: the kernels read them at several places and take what they read for the same.
+struct BatchRanges {
+    ByteRange r[3];
+    explicit BatchRanges(const BatchView &b)
+    {
+        r[0] = range_of(b.table, (size_t)b.n_seqs * b.width * 4);
+        r[1] = range_of(b.lens, (size_t)b.n_seqs * 4);
+        r[2] = range_of(b.q_start, ((size_t)b.n_seqs + 1) * 4);
+    }
+    bool hit(ByteRange x) const { return overlaps(x, r[0]) || overlaps(x, r[1]) || overlaps(x, r[2]); }
+};
+
+// From the first to the last byte of T rows of `len` elements of `size` bytes.
+inline ByteRange rows_range(const void *p, int64_t stride, int64_t len, int size, int64_t T)
 {
-    const ByteRange r = range_of(p, (size_t)bytes);
-    const size_t steps = (size_t)c.num_pages * c.n_kv_heads;
-    const size_t codes = steps * c.page_size * c.head_dim;
-    return overlaps(r, range_of(c.k, codes)) || overlaps(r, range_of(c.v, codes)) ||
-           overlaps(r, range_of(c.k_step, steps * 4)) || overlaps(r, range_of(c.v_step, steps * 4));
+    return range_of(p, (size_t)(((T - 1) * stride + len) * size));
 }
 
 template <bool F32, int D>
@@ -213,14 +246,22 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
     if (!q != !q_out || (rope && rope_len < 1)) return BITNET_ERR_INVALID_ARG;
     const int d = cache->head_dim, hk = cache->n_kv_heads;
     const int size = dtype == BITNET_DTYPE_F32 ? 4 : 2;
-    const int64_t kw = (int64_t)hk * d;
+    const int64_t kw = (int64_t)hk * d, T = a.bt.T;
     if ((st = check_rows(k, k_stride, kw, size)) != BITNET_OK || (st = check_rows(v, v_stride, kw, size)) != BITNET_OK)
         return st;
     if (rope && !aligned16(rope)) return BITNET_ERR_MISALIGNED;
+    // what is written (the cache, q_out) must not be what is read
+    const CacheRanges written(*cache);
+    const BatchRanges described(a.bt);
+    const ByteRange rr = rope ? range_of(rope, (size_t)std::min<int64_t>(rope_len, INT32_MAX) * d * 4) : ByteRange{0, 0};
+    if (!written.apart() || written.hit(rows_range(k, k_stride, kw, size, T)) ||
+        written.hit(rows_range(v, v_stride, kw, size, T)) || written.hit(rr) || described.hit(written.r[0]) ||
+        described.hit(written.r[1]) || described.hit(written.r[2]) || described.hit(written.r[3]))
+        return BITNET_ERR_INVALID_ARG;
     if (q) {
         if (n_heads < 1) return BITNET_ERR_INVALID_ARG;
         if (n_heads % hk != 0 || n_heads / hk > kMaxGroup) return BITNET_ERR_UNSUPPORTED_SHAPE;
-        const int64_t qw = (int64_t)n_heads * d, T = a.bt.T;
+        const int64_t qw = (int64_t)n_heads * d;
         if ((st = check_rows(q, q_stride, qw, size)) != BITNET_OK ||
             (st = check_rows(q_out, q_out_stride, qw, 2)) != BITNET_OK)
             return st;
@@ -228,8 +269,10 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
         if ((!same && rows_share(q, q_stride * size, qw * size, q_out, q_out_stride * 2, qw * 2, T)) ||
             rows_share(k, k_stride * size, kw * size, q_out, q_out_stride * 2, qw * 2, T) ||
             rows_share(v, v_stride * size, kw * size, q_out, q_out_stride * 2, qw * 2, T) ||
-            hits_cache(*cache, q_out, ((T - 1) * q_out_stride + qw) * 2))
+            written.hit(rows_range(q, q_stride, qw, size, T)))
             return BITNET_ERR_INVALID_ARG;
+        const ByteRange qo = rows_range(q_out, q_out_stride, qw, 2, T);
+        if (written.hit(qo) || described.hit(qo) || overlaps(qo, rr)) return BITNET_ERR_INVALID_ARG;
     }
     a.q = q;
     a.k = k;
@@ -282,11 +325,11 @@ bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv
         return BITNET_ERR_INVALID_ARG;
     if (!workspace || ws_bytes < p.total()) return BITNET_ERR_WORKSPACE;
     if (!aligned16(workspace)) return BITNET_ERR_MISALIGNED;
-    const ByteRange wr = range_of(workspace, p.total());
-    const int64_t out_bytes = ((int64_t)(a.bt.T - 1) * out_stride + qw) * 2;
-    if (overlaps(wr, range_of(out, (size_t)out_bytes)) ||
-        overlaps(wr, range_of(q, (size_t)(((int64_t)(a.bt.T - 1) * q_stride + qw) * 2))) ||
-        hits_cache(*cache, out, out_bytes) || hits_cache(*cache, workspace, (int64_t)p.total()))
+    const ByteRange wr = range_of(workspace, p.total()), written = rows_range(out, out_stride, qw, 2, a.bt.T);
+    const CacheRanges cached(*cache);
+    const BatchRanges described(a.bt);
+    if (overlaps(wr, written) || overlaps(wr, rows_range(q, q_stride, qw, 2, a.bt.T)) || cached.hit(written) ||
+        cached.hit(wr) || described.hit(written) || described.hit(wr))
         return BITNET_ERR_INVALID_ARG;
     const int dev = current_device();
     const int sms = num_sms_for(dev);
