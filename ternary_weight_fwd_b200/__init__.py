@@ -632,6 +632,8 @@ def bitnet_attention(cache, page_table, seq_lens, q_start, q, max_new, *, scale=
         workspace = _kv_empty(max(need, 16), torch.uint8, q.device, stream)
     elif workspace.get_device() != q.get_device():
         raise ValueError(f"workspace is on {workspace.device}, the cache on {q.device}")
+    elif not workspace.is_contiguous():  # its elements are then not its bytes: an expanded one has next to none
+        raise ValueError("workspace must be contiguous")
     _kv_call("bitnet_attention", kc.get_device(), stream, c, b, q.data_ptr(), qs, heads, max_new,
              d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
              workspace.numel() * workspace.element_size())
