@@ -39,12 +39,14 @@
  *
  * What only the device can see -- page ids, lengths, offsets, positions -- is
  * checked there: a page id outside [0, num_pages), a seq_lens[b] that is
- * negative, larger than table_width * page_size or smaller than n_b, a q_start
- * that decreases or leaves [0, T], a position beyond the rotation table, or more
- * new tokens than max_new makes the kernels skip what they would have had to
- * access and record BITNET_ERR_INVALID_ARG in the batch status word (see
- * bitnet_batch_status).  The outputs of the sequences concerned are then
- * unspecified; nothing outside the caller's buffers is touched.
+ * negative, larger than table_width * page_size or (append only) smaller than
+ * n_b, a q_start that decreases or leaves [0, T], a position beyond the rotation
+ * table, or more new tokens than max_new makes the kernels skip what they would
+ * have had to access and record BITNET_ERR_INVALID_ARG in the batch status word
+ * (see bitnet_batch_status).  The outputs of the sequences concerned are then
+ * unspecified; nothing outside the caller's buffers is touched.  A q_start that
+ * decreases may leave sequences that look sound and claim the same rows: if all
+ * together claim more than T, the attention for prompts computes none of them.
  */
 #ifndef BITNET_KV_H
 #define BITNET_KV_H
@@ -151,11 +153,18 @@ bitnet_status_t bitnet_kv_append(const bitnet_kv_cache_t *cache, const bitnet_kv
  *              bytes, any contents, apart from q, out, the cache and the batch;
  *              calls that may overlap on the GPU need separate ones
  *
- * Weights and sums of the softmax are fp32; its weights and the queries enter
- * the tensor cores in fp16 (11 bits, queries scaled by a power of two per row),
- * the codes exactly; products are summed in fp32 and the result is rounded to
- * bf16 once.  Results do not depend on timing: the same call gives the same
- * bits.
+ * Weights and sums of the softmax are fp32; its weights enter the tensor cores in
+ * fp16 (11 bits), the codes exactly, the queries in fp16 scaled by a power of two
+ * per row (few new tokens) or as they are (prompts); products are summed in fp32
+ * and the result is rounded to bf16 once.  Results do not depend on timing: the
+ * same call gives the same bits.
+ *
+ * Ranges.  For prompts a sum of D products of a query's elements and codes has to
+ * be finite in fp32 (always so below 2e34); for few tokens only the scores have
+ * to.  A sum of 2^8 |v| over the tokens has to be finite.  Steps of one sequence
+ * may lie any number of powers of two apart; what a page adds whose v_step is
+ * below 2^-90 of the sequence's largest, or below 2^-35 of the largest within the
+ * same 128 tokens, may be off by that fraction of the largest value.
  */
 bitnet_status_t bitnet_attention(const bitnet_kv_cache_t *cache, const bitnet_kv_batch_t *batch, const void *q,
                                  int64_t q_stride, int32_t n_heads, int32_t max_new, float scale, void *out,

@@ -4,9 +4,11 @@
 //
 // Same formulas as attention_tokens.cuh.  Bound by the tensor cores and the
 // exponentials: 4 D flops and one exp2 per visible (query head, token) pair.  As
-// built, a block of 128 tokens takes 4800 cycles: the softmax of an MMA tile (3000)
-// and its products (1700, queueing included) take turns, since weights lie over their
-// scores, and the two tiles hide each other only in part.
+// built, a block of 128 tokens takes a CTA 5200 cycles (2.66 us, from the times of 512
+// new tokens behind 16, 32 and 64 k cached ones; 2.6 us with D = 64), its four products
+// 2048 of them: softmax and products of an MMA tile take turns, since weights lie over
+// their scores, and the two tiles hide each other only in part (tensor pipe 36 % busy,
+// exponentials 38 %, half of the issue slots used).
 //
 // Query rows of a (sequence, kv head) are its new tokens times the query heads
 // of the group (row = token * group + head).  An MMA tile holds as many whole
@@ -20,7 +22,7 @@
 // contiguous shares, and tiles that two or more CTAs share are joined by
 // k_attention_prompt_join through the workspace, in the order of the CTAs.  (Equal
 // shares always: 144 us for a 4096-token prompt, the parts of 147 shared tiles
-// written and read again; now 131 us, 0.66 PFLOP/s of visible products.)  Which CTA
+// written and read again; now 128 us, 0.67 PFLOP/s of visible products.)  Which CTA
 // takes a tile does not change its result.
 //
 // One CTA, 24 warps:
@@ -428,6 +430,17 @@ BITNET_DEVINL float max3(float a, float b, float c)
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// 3-D tiled tensor copy global -> shared (no multicast); c0 times the element size a multiple of 16 bytes.
+BITNET_DEVINL void tma_load_3d(uint32_t dst_smem, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
+                               uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst_smem),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // Four codes -> two bf16 pairs (bytes 0, 1) and (2, 3): the low seven bits go

@@ -20,7 +20,7 @@
 // (Before, a producer warp fed all warps through one ring by TMA, and the warps
 // joined at the end of every row tile: 70 us for 64 sequences of up to 4096 tokens,
 // 51 us of them without any computation; 16-token pages, a TMA each, took longer
-// still.  Now, with the kernel's later steps: 45 us, 3.9 TB/s; one sequence of 131071
+// still.  Now, with the kernel's later steps: 45 us, 3.8 TB/s; one sequence of 131071
 // tokens 41 us, 4.1 TB/s, join included.)
 //
 // The products run on mma.sync m16n8k16 in fp16 with fp32 sums and the tokens
@@ -43,7 +43,7 @@ namespace bitnet {
 
 constexpr int AT_GROUP = 16;    // tokens a warp takes at a time (a page holds at least as many): a unit
 // Query rows per (sequence, kv head) that this kernel is chosen for.  Its cost grows with every
-// 16 rows, that of the kernel for prompts with every 256; measured with 48 and 64 rows: 64
+// 16 rows, that of the kernel for prompts with every 256; measured (D = 128) with 48 and 64 rows: 64
 // sequences of 2048 tokens 117 and 150 us here, 141 and 141 us there; with 64 rows 16 sequences
 // of 8192 tokens (8 query heads a kv head) 117 us here, 107 us there, 64 sequences of 300 tokens
 // 46 and 55 us.
@@ -93,17 +93,6 @@ constexpr int AT_BUFS = 2; // a warp's buffers of a group's codes (three: no fas
 constexpr __host__ __device__ int at_smem(int d, int nq)
 {
     return 4096 + at_warps(nq) * (AT_BUFS * 2 * AT_GROUP * d + 8 * nq * (d + 4) * 4 + 2 * 8 * nq * 8) + 1024;
-}
-
-// 3-D tiled tensor copy global -> shared (no multicast); c0 times the element size a multiple of 16 bytes.
-BITNET_DEVINL void tma_load_3d(uint32_t dst_smem, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
-                               uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst_smem),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-        : "memory");
 }
 
 BITNET_DEVINL void cp_async16_u32(uint32_t dst_smem, const void *src_gmem)

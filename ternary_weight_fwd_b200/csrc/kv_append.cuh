@@ -120,7 +120,7 @@ BITNET_DEVINL int ka_code(float x, float step)
 // inverse is within 127 * 3 * 2^-24 < 3e-5 of fl(x / step), so where it is not within 1e-4
 // of the middle between two integers both round alike; else (one set of sixteen in 300), and
 // for steps near the subnormal ones, the division itself decides.  (Dividing always: 81 us
-// for 17 k tokens of 16 heads, the divisions' units 35 % busy.)
+// for 17 k tokens of 16 heads.)
 BITNET_DEVINL void ka_codes(const float (&x)[16], float step, float inv, uint32_t (&w)[4])
 {
     constexpr float magic = 12582912.0f; // 1.5 * 2^23: the sum's low byte is the nearest integer
